@@ -221,7 +221,7 @@ def _verify(s):
     if s["draft"] is not None:
         less = s["draft"][at, i].double()
     else:
-        less = (torch.arange(V, device=DEV) == d[at, i][:, None]) * torch.inf
+        less = torch.where(torch.arange(V, device=DEV) == d[at, i][:, None], torch.inf, 0.0)
     w = torch.where(rejected, (w - less).clamp(min=0), w)
     w = torch.where(w.sum(1, keepdim=True) > 0, w, target[at, n].double())
     c = w.cumsum(1)
