@@ -10,6 +10,7 @@ there is no fallback: if the library is missing, the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -33,6 +34,10 @@ FMT_NVFP4 = 0
 FMT_FP8 = 1
 MAX_M = 16
 MAX_GROUP = 8
+MAX_EXPERTS = 512
+PROB_F16 = 0
+PROB_F32 = 1
+PROB_BF16 = 2
 
 _lock = threading.Lock()
 _lib = None
@@ -90,6 +95,18 @@ def library() -> ctypes.CDLL:
                 "skinny_stream_read": (ctypes.c_int, [p, sz, ctypes.c_int, p, p]),
                 "skinny_nvfp4_gemm_grouped": (ctypes.c_int, [ctypes.POINTER(GroupMember), ctypes.c_int,
                                                              ctypes.c_int, i64, ctypes.c_int, p, sz, p]),
+                "skinny_tile_workspace_bytes": (ctypes.c_int, [ctypes.POINTER(sz)]),
+                "skinny_experts_packed_bytes": (sz, [ctypes.c_int, i64, i64, i64, ctypes.c_int]),
+                "skinny_pack_experts": (ctypes.c_int, [ctypes.c_int, p, p, i64, i64, i64, ctypes.c_int, p, p]),
+                "skinny_gemm_experts": (ctypes.c_int, [ctypes.c_int, p, i64, i64, p, i64, p, p, i64, p, ctypes.c_int,
+                                                       p, sz, p]),
+                "skinny_gemm_experts_silu_mul": (ctypes.c_int, [ctypes.c_int, p, i64, i64, p, i64, p, p, i64, p,
+                                                                ctypes.c_int, p, sz, p]),
+                "skinny_quantize_int8": (ctypes.c_int, [p, ctypes.c_int, i64, i64, p, p, p]),
+                "skinny_int8_gemm": (ctypes.c_int, [p, p, i64, i64, p, p, i64, p, ctypes.c_int, p, sz, p]),
+                "skinny_tile_device_error": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_uint)]),
+                "skinny_verify_draft": (ctypes.c_int, [p, i64, i64, p, i64, i64, ctypes.c_int, p, p, p, i64, i64, i64,
+                                                       p, p, p]),
                 "skinny_debug_static_workspace_address": (ctypes.c_int, [ctypes.POINTER(ctypes.c_void_p)]),
             }
             for name, (res, args) in sigs.items():
@@ -429,3 +446,346 @@ def device_error(clear: bool = True) -> int:
     v = ctypes.c_uint(0)
     _check(library().skinny_device_error(1 if clear else 0, ctypes.byref(v)), "skinny_device_error")
     return int(v.value)
+
+
+# ---------------------------------------------------------------------------
+# Products for any number of tokens: experts and 8-bit integers
+# ---------------------------------------------------------------------------
+
+@contextlib.contextmanager
+def _on(device, *tensors):
+    """Makes `device` current for a call; every tensor must be on it."""
+    import torch
+
+    if device.type != "cuda":
+        raise ValueError("tensors on a CUDA device expected, got %s" % device)
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("tensors on one device expected: %s and %s" % (device, t.device))
+    if device.index is None or device.index == torch.cuda.current_device():
+        yield
+    else:
+        with torch.cuda.device(device):
+            yield
+
+
+def _ws(workspace):
+    if workspace is None:
+        return None, 0
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _out_code(y, shape, what):
+    import torch
+
+    if tuple(y.shape) != tuple(shape) or not y.is_contiguous() or y.dtype not in (torch.float16, torch.float32):
+        raise ValueError("%s must be a contiguous float16/float32 %s tensor" % (what, list(shape)))
+    return OUT_F32 if y.dtype == torch.float32 else OUT_F16
+
+
+def tile_workspace_bytes() -> int:
+    """Size of the experts' and int8 products' workspace on the current device."""
+    b = ctypes.c_size_t(0)
+    _check(library().skinny_tile_workspace_bytes(ctypes.byref(b)), "skinny_tile_workspace_bytes")
+    return int(b.value)
+
+
+def make_experts_workspace(device="cuda"):
+    """A zero-filled workspace for gemm_experts and gemm_experts_silu_mul; it
+    serves calls of any shape in turn, but not two that can run at the same time."""
+    import torch
+
+    device = torch.device(device)
+    with _on(device):
+        return torch.zeros(tile_workspace_bytes(), dtype=torch.uint8, device=device)
+
+
+def make_int8_workspace(device="cuda"):
+    """A zero-filled workspace for gemm_int8 (alike, and interchangeable with, make_experts_workspace's)."""
+    return make_experts_workspace(device)
+
+
+def _pack_experts(fmt, codes, scales, E, N, K, gate_up):
+    import torch
+
+    nb = int(library().skinny_experts_packed_bytes(fmt, E, N, K, int(gate_up)))
+    if nb == 0:
+        raise SkinnyError(ERR_INVALID_ARG, "pack_experts shape")
+    with _on(codes.device, scales):
+        out = torch.empty(nb, dtype=torch.uint8, device=codes.device)
+        st = library().skinny_pack_experts(fmt, codes.data_ptr(), scales.data_ptr() if scales is not None else None,
+                                           E, N, K, int(gate_up), out.data_ptr(), _stream_handle(None))
+        _check(st, "skinny_pack_experts")
+    return out
+
+
+def _device_tensor(a, dtype, device):
+    import torch
+
+    t = a if isinstance(a, torch.Tensor) else torch.from_numpy(np.ascontiguousarray(a))
+    if t.dtype != dtype:
+        raise ValueError("a %s tensor expected, got %s" % (dtype, t.dtype))
+    return t.to(device).contiguous()
+
+
+@dataclasses.dataclass
+class PackedExpertsNVFP4:
+    """E experts of N x K NVFP4 weights, packed for gemm_experts or (gate_up:
+    rows 0..N/2-1 gate, N/2..N-1 up) for gemm_experts_silu_mul."""
+    data: "object"           # torch.uint8 device tensor
+    scale: "object"          # torch.float32 device tensor [E]: one scale per expert
+    E: int
+    N: int
+    K: int
+    gate_up: bool
+
+    @classmethod
+    def from_logical(cls, codes, scales, expert_scale, gate_up=False, device="cuda"):
+        """codes [E, N, K/2] uint8 (low nibble = even k), scales [E, N, K/16]
+        UE4M3 bytes, expert_scale [E] float32; numpy arrays or torch tensors."""
+        import torch
+
+        codes, scales = (_device_tensor(a, torch.uint8, device) for a in (codes, scales))
+        expert_scale = _device_tensor(expert_scale, torch.float32, device)
+        if codes.dim() != 3:
+            raise ValueError("codes must be [E, N, K/2]")
+        E, N, K = codes.shape[0], codes.shape[1], codes.shape[2] * 2
+        if tuple(scales.shape) != (E, N, K // 16) or tuple(expert_scale.shape) != (E,):
+            raise ValueError("scales must be [E, N, K/16] and expert_scale [E]")
+        if bool((scales >= 0x7F).any()):
+            raise ValueError("block scales must be finite non-negative UE4M3 bytes")
+        return cls(_pack_experts(FMT_NVFP4, codes, scales, E, N, K, gate_up), expert_scale, E, N, K, bool(gate_up))
+
+    @property
+    def fmt(self) -> int:
+        return FMT_NVFP4
+
+
+@dataclasses.dataclass
+class PackedExpertsFP8:
+    """E experts of N x K FP8 E4M3 weights with a scale per expert and output
+    channel, packed as PackedExpertsNVFP4."""
+    data: "object"           # torch.uint8 device tensor
+    scale: "object"          # torch.float32 device tensor [E, N]
+    E: int
+    N: int
+    K: int
+    gate_up: bool
+
+    @classmethod
+    def from_logical(cls, q, channel_scale, gate_up=False, device="cuda"):
+        """q [E, N, K] E4M3 bytes (uint8), channel_scale [E, N] float32."""
+        import torch
+
+        q = _device_tensor(q, torch.uint8, device)
+        channel_scale = _device_tensor(channel_scale, torch.float32, device)
+        if q.dim() != 3 or tuple(channel_scale.shape) != tuple(q.shape[:2]):
+            raise ValueError("q must be [E, N, K] and channel_scale [E, N]")
+        if bool(((q & 0x7F) == 0x7F).any()):
+            raise ValueError("E4M3 codes must not be NaN")
+        E, N, K = q.shape
+        return cls(_pack_experts(FMT_FP8, q, None, E, N, K, gate_up), channel_scale, E, N, K, bool(gate_up))
+
+    @property
+    def fmt(self) -> int:
+        return FMT_FP8
+
+
+def _gemm_experts(y, x, w, offsets, workspace, stream, silu):
+    import torch
+
+    if w.gate_up != silu:
+        raise TypeError("gemm_experts takes experts packed without gate_up, gemm_experts_silu_mul with it")
+    if x.dim() != 2 or x.dtype != torch.float16 or not x.is_contiguous() or x.shape[1] != w.K:
+        raise ValueError("x must be a contiguous float16 [T, %d] tensor" % w.K)
+    if tuple(offsets.shape) != (w.E + 1,) or offsets.dtype != torch.int32 or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int32 [%d] tensor" % (w.E + 1))
+    T = x.shape[0]
+    outputs = w.N // 2 if silu else w.N
+    out = _out_code(y, (T, outputs), "y")
+    ws_ptr, ws_bytes = _ws(workspace)
+    name = "skinny_gemm_experts_silu_mul" if silu else "skinny_gemm_experts"
+    with _on(x.device, y, w.data, w.scale, offsets, workspace):
+        st = getattr(library(), name)(w.fmt, x.data_ptr(), T, w.K, offsets.data_ptr(), w.E, w.data.data_ptr(),
+                                      w.scale.data_ptr(), outputs, y.data_ptr(), out, ws_ptr, ws_bytes,
+                                      _stream_handle(stream))
+    _check(st, name)
+
+
+def gemm_experts_into(y, x, w, offsets, workspace=None, stream=None) -> None:
+    """y[r, N] = x[r, K] . W_e^T for the rows offsets[e] <= r < offsets[e+1] of
+    every expert e.  x float16 [T, K], sorted by expert; offsets int32 [E+1] on
+    the device; y float16 or float32, preallocated: rows of no expert are left
+    as they are.  T may be any number."""
+    _gemm_experts(y, x, w, offsets, workspace, stream, False)
+
+
+def gemm_experts(x, w, offsets, out_dtype=None, workspace=None, stream=None):
+    """Allocate y [T, N] (float16 unless out_dtype says otherwise): see
+    gemm_experts_into.  Rows of no expert are not written."""
+    import torch
+
+    y = torch.empty((x.shape[0], w.N), dtype=out_dtype or torch.float16, device=x.device)
+    gemm_experts_into(y, x, w, offsets, workspace=workspace, stream=stream)
+    return y
+
+
+def gemm_experts_silu_mul_into(y, x, w, offsets, workspace=None, stream=None) -> None:
+    """y[r, N/2] = silu(gate) * up of the rows' experts (packed with gate_up):
+    otherwise as gemm_experts_into."""
+    _gemm_experts(y, x, w, offsets, workspace, stream, True)
+
+
+def gemm_experts_silu_mul(x, w, offsets, out_dtype=None, workspace=None, stream=None):
+    """Allocate y [T, N/2]: see gemm_experts_silu_mul_into."""
+    import torch
+
+    y = torch.empty((x.shape[0], w.N // 2), dtype=out_dtype or torch.float16, device=x.device)
+    gemm_experts_silu_mul_into(y, x, w, offsets, workspace=workspace, stream=stream)
+    return y
+
+
+@dataclasses.dataclass
+class WeightInt8:
+    """N x K 8-bit integer weights, as they are, with one scale per output channel."""
+    codes: "object"          # torch.int8 device tensor [N, K]
+    channel_scale: "object"  # torch.float32 device tensor [N]
+
+    def __post_init__(self):
+        import torch
+
+        if self.codes.dim() != 2 or self.codes.dtype != torch.int8 or not self.codes.is_contiguous():
+            raise ValueError("codes must be a contiguous int8 [N, K] tensor")
+        s = self.channel_scale
+        if tuple(s.shape) != (self.codes.shape[0],) or s.dtype != torch.float32 or not s.is_contiguous():
+            raise ValueError("channel_scale must be a contiguous float32 [N] tensor")
+
+    @property
+    def N(self) -> int:
+        return int(self.codes.shape[0])
+
+    @property
+    def K(self) -> int:
+        return int(self.codes.shape[1])
+
+
+def quantize_int8_into(q, row_scale, x, stream=None) -> None:
+    """Rows of x (float16 or float32 [M, K]) to 8-bit integers: row_scale =
+    max|x| / 127, q = round(x / row_scale).  q int8 [M, K], row_scale float32 [M]."""
+    import torch
+
+    if x.dim() != 2 or x.dtype not in (torch.float16, torch.float32) or not x.is_contiguous():
+        raise ValueError("x must be a contiguous float16/float32 [M, K] tensor")
+    if q.shape != x.shape or q.dtype != torch.int8 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous int8 tensor of x's shape")
+    M, K = x.shape
+    if tuple(row_scale.shape) != (M,) or row_scale.dtype != torch.float32 or not row_scale.is_contiguous():
+        raise ValueError("row_scale must be a contiguous float32 [M] tensor")
+    with _on(x.device, q, row_scale):
+        st = library().skinny_quantize_int8(x.data_ptr(), OUT_F32 if x.dtype == torch.float32 else OUT_F16, M, K,
+                                            q.data_ptr(), row_scale.data_ptr(), _stream_handle(stream))
+    _check(st, "skinny_quantize_int8")
+
+
+def quantize_int8(x, stream=None):
+    """Allocate and return (q int8 [M, K], row_scale float32 [M]): see quantize_int8_into."""
+    import torch
+
+    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    row_scale = torch.empty(x.shape[:1], dtype=torch.float32, device=x.device)
+    quantize_int8_into(q, row_scale, x, stream=stream)
+    return q, row_scale
+
+
+def gemm_int8_into(y, q, row_scale, w: "WeightInt8", workspace=None, stream=None) -> None:
+    """y[m, n] = (q[m] . w[n]) * row_scale[m] * channel_scale[n], the sum exact
+    (y float16 or float32, preallocated; any number of rows)."""
+    import torch
+
+    if q.dim() != 2 or q.dtype != torch.int8 or not q.is_contiguous() or q.shape[1] != w.K:
+        raise ValueError("q must be a contiguous int8 [M, %d] tensor" % w.K)
+    M = q.shape[0]
+    if tuple(row_scale.shape) != (M,) or row_scale.dtype != torch.float32 or not row_scale.is_contiguous():
+        raise ValueError("row_scale must be a contiguous float32 [M] tensor")
+    out = _out_code(y, (M, w.N), "y")
+    ws_ptr, ws_bytes = _ws(workspace)
+    with _on(q.device, y, row_scale, w.codes, w.channel_scale, workspace):
+        st = library().skinny_int8_gemm(q.data_ptr(), row_scale.data_ptr(), M, w.K, w.codes.data_ptr(),
+                                        w.channel_scale.data_ptr(), w.N, y.data_ptr(), out, ws_ptr, ws_bytes,
+                                        _stream_handle(stream))
+    _check(st, "skinny_int8_gemm")
+
+
+def gemm_int8(q, row_scale, w: "WeightInt8", out_dtype=None, workspace=None, stream=None):
+    """Allocate y [M, N] (float16 unless out_dtype says otherwise): see gemm_int8_into."""
+    import torch
+
+    y = torch.empty((q.shape[0], w.N), dtype=out_dtype or torch.float16, device=q.device)
+    gemm_int8_into(y, q, row_scale, w, workspace=workspace, stream=stream)
+    return y
+
+
+def tile_device_error(clear: bool = True) -> int:
+    """As device_error, for the experts' and int8 products."""
+    v = ctypes.c_uint(0)
+    _check(library().skinny_tile_device_error(1 if clear else 0, ctypes.byref(v)), "skinny_tile_device_error")
+    return int(v.value)
+
+
+# ---------------------------------------------------------------------------
+# Verification of drafted tokens
+# ---------------------------------------------------------------------------
+
+def verify_draft_into(tokens, accepted, target, draft, draft_tokens, uniform, num_drafts=None, stream=None) -> None:
+    """A verify round against the target's probabilities, from given random
+    numbers: draft i of a request is accepted while uniform[i] * q_i(d_i) <
+    p_i(d_i); the next token is drawn from max(p - q, 0) at the first draft that
+    is not accepted, or from the last row of p, with uniform[S].
+
+    target        [B, S+1, V] float32, float16 or bfloat16; unit stride along V
+    draft         [B, S, V] of target's dtype, or None (drafts without a distribution)
+    draft_tokens  int32 [B, S];  uniform  float32 [B, S+1] in [0, 1)
+    num_drafts    int32 [B], or None for S each
+    tokens        int32 [B, S+1]: accepted drafts, the drawn token, then -1
+    accepted      int32 [B]
+    """
+    import torch
+
+    kinds = {torch.float16: PROB_F16, torch.float32: PROB_F32, torch.bfloat16: PROB_BF16}
+    if target.dim() != 3 or target.dtype not in kinds or target.shape[1] < 1 or target.shape[2] < 1:
+        raise ValueError("target must be a float32/float16/bfloat16 [B, S+1, V] tensor")
+    B, S, V = target.shape[0], target.shape[1] - 1, target.shape[2]
+    if V > 1 and target.stride(2) != 1:
+        raise ValueError("target must have unit stride along V")
+    if draft is not None:
+        if tuple(draft.shape) != (B, S, V) or draft.dtype != target.dtype:
+            raise ValueError("draft must be a [%d, %d, %d] tensor of target's dtype" % (B, S, V))
+        if V > 1 and draft.stride(2) != 1:
+            raise ValueError("draft must have unit stride along V")
+    for t, shape, dtype, what in ((draft_tokens, (B, S), torch.int32, "draft_tokens"),
+                                  (uniform, (B, S + 1), torch.float32, "uniform"),
+                                  (num_drafts, (B,), torch.int32, "num_drafts"),
+                                  (tokens, (B, S + 1), torch.int32, "tokens"), (accepted, (B,), torch.int32, "accepted")):
+        if t is None and what == "num_drafts":
+            continue
+        if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous %s %s tensor" % (what, dtype, list(shape)))
+    with _on(target.device, draft, draft_tokens, uniform, num_drafts, tokens, accepted):
+        has = draft is not None and S > 0
+        st = library().skinny_verify_draft(
+            target.data_ptr(), target.stride(0), target.stride(1), draft.data_ptr() if has else None,
+            draft.stride(0) if has else 0, draft.stride(1) if has else 0, kinds[target.dtype],
+            draft_tokens.data_ptr() if S else None, uniform.data_ptr(),
+            num_drafts.data_ptr() if num_drafts is not None else None, B, S, V, tokens.data_ptr(),
+            accepted.data_ptr(), _stream_handle(stream))
+    _check(st, "skinny_verify_draft")
+
+
+def verify_draft(target, draft, draft_tokens, uniform, num_drafts=None, stream=None):
+    """Allocate and return (tokens int32 [B, S+1], accepted int32 [B]): see verify_draft_into."""
+    import torch
+
+    tokens = torch.empty(target.shape[:2], dtype=torch.int32, device=target.device)
+    accepted = torch.empty(target.shape[:1], dtype=torch.int32, device=target.device)
+    verify_draft_into(tokens, accepted, target, draft, draft_tokens, uniform, num_drafts, stream=stream)
+    return tokens, accepted

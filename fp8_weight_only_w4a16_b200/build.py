@@ -12,8 +12,10 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-SOURCES = [os.path.join(CSRC, "skinny.cu"), os.path.join(CSRC, "stream_read.cu"), os.path.join(CSRC, "pack.cpp")]
-HEADERS = [os.path.join(CSRC, "layout.h"), os.path.join(CSRC, "ptx.cuh"), os.path.join(ROOT, "include", "skinny.h")]
+SOURCES = [os.path.join(CSRC, f) for f in ("skinny.cu", "stream_read.cu", "tile_gemm.cu", "quantize.cu", "verify.cu",
+                                           "pack.cpp")]
+HEADERS = [os.path.join(CSRC, "layout.h"), os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "tcgen05.cuh"),
+           os.path.join(ROOT, "include", "skinny.h")]
 LIBRARY = os.path.join(PKG, "libskinny.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

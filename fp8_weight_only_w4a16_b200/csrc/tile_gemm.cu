@@ -1,0 +1,997 @@
+// tile_gemm.cu -- tcgen05 GEMMs for any number of tokens:
+//
+//   experts:  y[r] = x[r] . W_e^T for the rows r of expert e (rows sorted by
+//             expert, ragged), W_e packed NVFP4 or FP8, x FP16;
+//   int8:     y[m][n] = (sum_k q[m][k] c[n][k]) * row_scale[m] * channel_scale[n].
+//
+// One kernel serves both.  The weights are the 128 rows of the matrix
+// instruction and the tokens its columns, so one token costs 16 columns and
+// a long batch 256, and the same kernel runs from one row to many thousands.
+// Per CTA (one per SM, persistent):
+//
+//   W producer   one thread, bulk copies of packed 128 x 128 blocks (experts)
+//                or tiled TMA boxes of the plain [N][K] matrix (int8);
+//   x producer   one thread, tiled TMA boxes of the activations;
+//   decoders     eight warps (experts only): a thread owns one weight row of
+//                the block and writes its 64 decoded FP16 values straight
+//                into tensor memory, from where the matrix instruction reads
+//                operand A.  The decoded weights never pass through shared
+//                memory, whose bandwidth would not carry them at the rate
+//                the codes arrive from HBM (2 bytes written and 2 read per
+//                weight against 0.56 bytes of HBM traffic).
+//   MMA          one thread issues tcgen05.mma into FP32 (int8: S32) accumulators;
+//   epilogue     four warps: a thread owns one output channel.
+//
+// Every product is exact (e2m1 * ue4m3 and e4m3 fit FP16, s8 * s8 fits S32);
+// the FP32 sums round as the tensor core's accumulator does, the S32 sums not
+// at all.  The scales are applied to the finished sum in FP32, and the output
+// is rounded once.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <mutex>
+
+#include "../../include/skinny.h"
+#include "tcgen05.cuh"
+
+namespace skinny {
+namespace {
+
+constexpr int kRows = 128;            // weight rows per tile: the lanes of tensor memory
+constexpr int kBlockK = 128;          // columns per packed block
+constexpr int kFmtInt8 = 2;           // next to SKINNY_FMT_NVFP4 and SKINNY_FMT_FP8
+constexpr int kMaxExperts = SKINNY_MAX_EXPERTS;
+constexpr int kMaxDevices = 64;
+constexpr int kSlotWords = kRows * 256;   // one CTA's partial tile in the workspace
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+
+// Bits of g_tile_error: which bounded wait gave up.
+constexpr unsigned kErrRing = 1u;         // a full or empty ring slot
+constexpr unsigned kErrAccumulator = 2u;  // an accumulator to be filled or drained
+constexpr unsigned kErrPartial = 4u;      // another CTA's partial sums
+
+__device__ unsigned int g_tile_error;
+
+// A slot's flag in the workspace: its low byte counts the epilogue warps that
+// have published their rows, the rest (in units of kRead) those that have read
+// them.  Zero between calls.
+constexpr unsigned kPublishedMask = 0xFF, kRead = 0x100;
+
+// Bytes of one packed 128 x 128 block.  A decoder thread reads its 64 columns
+// as 16-byte words, 128 rows side by side (no bank conflicts):
+//   NVFP4  [half][2 words][128 rows][32 codes], then [half][128 rows][4 block scales]
+//   FP8    [half][4 words][128 rows][16 codes]
+__host__ __device__ constexpr int block_bytes(int fmt) { return fmt == SKINNY_FMT_NVFP4 ? 9216 : 16384; }
+constexpr int kNvfp4BlockScales = 8192;
+
+struct Params {
+    const uint8_t* w;            // packed blocks (experts)
+    const float* scale;          // NVFP4 [E]; FP8 [E][N]; int8 [N]
+    const float* row_scale;      // int8 [T]
+    const int32_t* offsets;      // experts [E + 1]
+    void* y;                     // [T][outputs]
+    unsigned* partials;          // workspace: [P][kSlotWords], then [P] flags (or null)
+    unsigned* flags;
+    int T, N, E;
+    int G, C;                    // row tiles, K blocks
+    int outputs;                 // outputs per token: N, or N / 2 (SiLU*mul)
+    int out_f32;
+};
+
+template <int FMT, int TN>
+struct Cfg {
+    static constexpr bool kInt8 = FMT == kFmtInt8;
+    static constexpr int kWBytes = block_bytes(FMT);
+    static constexpr int kXPerBlock = kInt8 ? 1 : 2;         // 128-byte wide token boxes per K block
+    static constexpr int kXBytes = TN * 128;
+    static constexpr int kBox = TN <= 32 ? 16 : TN / 4;      // tokens per TMA box
+    static constexpr int kAStages = kInt8 ? 0 : 4;           // decoded blocks in tensor memory, 64 columns each
+    static constexpr int kACol = 256;
+    // Accumulators: two when they fit next to the decoded blocks.
+    static constexpr int kDStages = (kInt8 || TN <= 128) ? 2 : 1;
+    static constexpr int kDecodeWarps = kInt8 ? 0 : 8;
+    static constexpr int kWarps = 4 + kDecodeWarps + 4;
+    static constexpr int kThreads = kWarps * 32;
+    // Ring slots: the tokens' ring holds at least two K blocks, the weights'
+    // ring takes what is left.
+    static constexpr int kBudget = 218 * 1024;
+    static constexpr int kXStages = kInt8 ? (kBudget / (kXBytes + kWBytes) < 12 ? kBudget / (kXBytes + kWBytes) : 12)
+                                          : (TN <= 32 ? 16 : TN <= 128 ? 6 : 4);
+    static constexpr int kWFit = (kBudget - kXStages * kXBytes) / kWBytes;
+    static constexpr int kWStages = kInt8 ? kXStages : (kWFit < 16 ? kWFit : 16);
+    static constexpr int kXOff = 0;
+    static constexpr int kWOff = kXStages * kXBytes;
+    static constexpr int kBarOff = kWOff + kWStages * kWBytes;
+    static constexpr int kBars = 2 * (kXStages + kWStages + kAStages + kDStages) + 1;
+    static constexpr int kBytes = kBarOff + kBars * 8 + 1024;   // + alignment of the dynamic shared memory
+    static_assert(kBytes + 8 * (kMaxExperts + 2) + 256 <= 232448, "shared memory per CTA");
+    static_assert(kDStages * TN <= kACol || kInt8, "accumulators and decoded blocks overlap");
+    static_assert(kDStages * TN <= 512 && kACol + 64 * kAStages <= 512, "tensor memory");
+};
+
+// The tile sequence, from the experts' row counts: expert e has
+// ceil(rows / TN) token tiles of q_e rows each (a multiple of 16, so the
+// tiles of one expert are alike) times G row tiles.
+struct Schedule {
+    int tiles[kMaxExperts + 1];          // running number of tiles
+    int rows[kMaxExperts + 1];           // running row offset (offsets made monotone and clamped to [0, T])
+    uint32_t warp_tot_tiles[16];
+    int warp_max[16];
+    int total;
+    uint32_t tmem;
+    int abort;
+};
+
+__device__ __forceinline__ int token_tiles(int rows, int TN) { return (rows + TN - 1) / TN; }
+__device__ __forceinline__ int tile_rows(int rows, int nt) { return ((rows + nt - 1) / nt + 15) & ~15; }
+
+// Largest e with a[e] <= v, 0 <= e < n (a[0] = 0, a ascending).
+__device__ __forceinline__ int find(const int* a, int n, int v)
+{
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= v) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// A piece of one CTA's work: K blocks [k0, k1) of a tile.
+struct Segment {
+    int e, row_tile, t0, n;   // expert, row tile, first token row, token rows
+    int tile, k0, k1;
+};
+
+// The CTA's pieces.  Few tiles are split along K so that every CTA streams
+// the same number of blocks (contiguous ranges of the tile sequence's blocks,
+// walked backwards: the partial sums that other CTAs wait for come first);
+// many tiles are dealt out whole, one after another, so that the CTAs work
+// on neighbouring tiles and share their operands in L2.
+template <int TN>
+struct Walk {
+    const Schedule& s;
+    const Params& p;
+    bool split;
+    int u0, u;       // split: first block, and one past the next piece's last
+    int tile;        // whole tiles: the next one
+
+    __device__ static bool use_split(const Schedule& s, const Params& p)
+    {
+        // From eight tiles per CTA on, the last round's idle CTAs cost less
+        // than the exchange of partial sums.
+        return p.partials != nullptr && s.total < 8 * (int)gridDim.x;
+    }
+    __device__ static int start(const Schedule& s, const Params& p, int b)
+    {
+        return (int)((int64_t)b * s.total * p.C / (int)gridDim.x);
+    }
+    __device__ Walk(const Schedule& s_, const Params& p_) : s(s_), p(p_)
+    {
+        split = use_split(s, p);
+        if (split) {
+            u0 = start(s, p, blockIdx.x);
+            u = start(s, p, blockIdx.x + 1);
+        } else {
+            tile = blockIdx.x;
+        }
+    }
+    __device__ bool next(Segment& g)
+    {
+        if (split) {
+            if (u <= u0) return false;
+            g.tile = (u - 1) / p.C;
+            g.k1 = u - g.tile * p.C;
+            g.k0 = u0 > g.tile * p.C ? u0 - g.tile * p.C : 0;
+            u = g.tile * p.C + g.k0;
+        } else {
+            if (tile >= s.total) return false;
+            g.tile = tile;
+            g.k0 = 0;
+            g.k1 = p.C;
+            tile += gridDim.x;
+        }
+        g.e = find(s.tiles, p.E, g.tile);
+        const int m = s.rows[g.e + 1] - s.rows[g.e];
+        const int q = tile_rows(m, token_tiles(m, TN));
+        const int lt = g.tile - s.tiles[g.e];
+        g.row_tile = lt % p.G;
+        const int t = lt / p.G * q;
+        g.t0 = s.rows[g.e] + t;
+        g.n = m - t < q ? m - t : q;
+        return true;
+    }
+};
+
+// A ring position.
+struct Ring {
+    int i = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step(int n)
+    {
+        if (++i == n) {
+            i = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned code)
+{
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if ((i & 15u) == 0) {
+            if (*abort) return false;
+            if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+                *abort = 1;
+                atomicOr(&g_tile_error, code);
+                return false;
+            }
+        }
+    }
+}
+
+// False once any wait of the CTA has given up: every role then stops.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort, unsigned code)
+{
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    return wait_slow(bar, parity, abort, code);
+}
+
+// Waits for a ring's copies in flight (the last `issued`, at most one round).
+__device__ __noinline__ void drain(Ring r, int issued, int stages, uint64_t* full)
+{
+    for (int k = issued < stages ? issued : stages; k > 0; --k) {
+        if (r.i == 0) {
+            r.i = stages;
+            r.phase ^= 1;
+        }
+        --r.i;
+        ptx::mbar_wait(full + r.i, r.phase, kWaitLimitNs);
+    }
+}
+
+template <int FMT, int TN>
+struct Shared {
+    using C = Cfg<FMT, TN>;
+    uint8_t* base;
+    __device__ uint8_t* x(int i) const { return base + C::kXOff + i * C::kXBytes; }
+    __device__ uint8_t* w(int i) const { return base + C::kWOff + i * C::kWBytes; }
+    __device__ uint64_t* bars() const { return reinterpret_cast<uint64_t*>(base + C::kBarOff); }
+    __device__ uint64_t* x_full(int i) const { return bars() + i; }
+    __device__ uint64_t* x_empty(int i) const { return bars() + C::kXStages + i; }
+    __device__ uint64_t* w_full(int i) const { return bars() + 2 * C::kXStages + i; }
+    __device__ uint64_t* w_empty(int i) const { return bars() + 2 * C::kXStages + C::kWStages + i; }
+    __device__ uint64_t* a_full(int i) const { return bars() + 2 * (C::kXStages + C::kWStages) + i; }
+    __device__ uint64_t* a_empty(int i) const { return a_full(i) + C::kAStages; }
+    __device__ uint64_t* d_full(int i) const { return bars() + 2 * (C::kXStages + C::kWStages + C::kAStages) + i; }
+    __device__ uint64_t* d_empty(int i) const { return d_full(i) + C::kDStages; }
+    __device__ uint64_t* drained() const { return bars() + C::kBars - 1; }
+};
+
+// Inclusive running maximum / sum over the block's threads' values.
+__device__ __forceinline__ int warp_scan_max(int v)
+{
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int o = __shfl_up_sync(~0u, v, d);
+        if ((threadIdx.x & 31) >= d) v = v > o ? v : o;
+    }
+    return v;
+}
+__device__ __forceinline__ uint32_t warp_scan_add(uint32_t v)
+{
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const uint32_t o = __shfl_up_sync(~0u, v, d);
+        if ((threadIdx.x & 31) >= d) v += o;
+    }
+    return v;
+}
+
+// The experts' schedule, by the whole block (512 threads, one expert each).
+// Offsets are device data that the host has not seen: they are clamped to
+// [0, T] and made non-decreasing, so no row is outside x and y or has two experts.
+template <int TN>
+__device__ void make_schedule(Schedule& s, const Params& p)
+{
+    const int i = threadIdx.x, w = i / 32;
+    auto clamp = [&](int v) { return v < 0 ? 0 : v > p.T ? p.T : v; };
+    const int first = clamp(p.offsets[0]);
+    int v = i < p.E ? clamp(p.offsets[i + 1]) : 0;
+    v = v > first ? v : first;
+    v = warp_scan_max(v);
+    if ((i & 31) == 31) s.warp_max[w] = v;
+    __syncthreads();
+    for (int k = 0; k < w; ++k) v = v > s.warp_max[k] ? v : s.warp_max[k];
+    if (i == 0) s.rows[0] = first;
+    if (i < p.E) s.rows[i + 1] = v;
+    __syncthreads();
+    uint32_t n = i < p.E ? (uint32_t)token_tiles(s.rows[i + 1] - s.rows[i], TN) * (uint32_t)p.G : 0;
+    n = warp_scan_add(n);
+    if ((i & 31) == 31) s.warp_tot_tiles[w] = n;
+    __syncthreads();
+    for (int k = 0; k < w; ++k) n += s.warp_tot_tiles[k];
+    if (i == 0) s.tiles[0] = 0;
+    if (i < p.E) s.tiles[i + 1] = (int)n;
+    if (i == p.E - 1) s.total = (int)n;
+}
+
+__device__ __forceinline__ void store_out(void* y, int64_t at, float v, int f32)
+{
+    if (f32) static_cast<float*>(y)[at] = v;
+    else static_cast<__half*>(y)[at] = __float2half_rn(v);
+}
+
+template <int FMT, int TN, bool SILU>
+__global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
+    tile_gemm(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap x_map,
+              const __grid_constant__ CUtensorMap w_map)
+{
+    using C = Cfg<FMT, TN>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Schedule s;
+    const Shared<FMT, TN> sm{smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u)};
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kXStages; ++i) {
+            ptx::mbar_init(sm.x_full(i), 1);
+            ptx::mbar_init(sm.x_empty(i), 1);
+        }
+        for (int i = 0; i < C::kWStages; ++i) {
+            ptx::mbar_init(sm.w_full(i), 1);
+            ptx::mbar_init(sm.w_empty(i), C::kInt8 ? 1 : C::kDecodeWarps);
+        }
+        for (int i = 0; i < C::kAStages; ++i) {
+            ptx::mbar_init(sm.a_full(i), C::kDecodeWarps);
+            ptx::mbar_init(sm.a_empty(i), 1);
+        }
+        for (int i = 0; i < C::kDStages; ++i) {
+            ptx::mbar_init(sm.d_full(i), 1);
+            ptx::mbar_init(sm.d_empty(i), 4);
+        }
+        ptx::mbar_init(sm.drained(), 1);
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&x_map);
+        if (C::kInt8) ptx::prefetch_tensormap(&w_map);
+        s.abort = 0;
+    }
+    if (warp == 2) ptx::tmem_alloc_all(&s.tmem);
+    ptx::pdl_launch_dependents();
+    if constexpr (C::kInt8) {
+        // The schedule needs nothing of the previous kernel: only the roles
+        // that touch its results wait for it.
+        if (threadIdx.x == 0) {
+            s.rows[0] = 0;
+            s.rows[1] = p.T;
+            s.tiles[0] = 0;
+            s.tiles[1] = s.total = token_tiles(p.T, TN) * p.G;
+        }
+    } else {
+        ptx::pdl_wait_prior_grid();
+        make_schedule<TN>(s, p);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    Walk<TN> walk(s, p);
+    Segment g;
+    Ring r;            // the producers' position and how much they have issued
+    int issued = 0;
+
+    if (warp == 0) {
+        // ---- W producer
+        if (lane == 0) {
+            bool ok = true;
+            const uint64_t pol = TN <= 32 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
+            while (ok && walk.next(g)) {
+                const uint8_t* src =
+                    C::kInt8 ? nullptr : p.w + ((size_t)g.e * p.G + g.row_tile) * p.C * C::kWBytes;
+                for (int k = g.k0; k < g.k1; ++k) {
+                    if (!wait(sm.w_empty(r.i), r.phase ^ 1, &s.abort, kErrRing)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::mbar_arrive_expect_tx(sm.w_full(r.i), C::kWBytes);
+                    if constexpr (C::kInt8)
+                        ptx::tma_load_2d(sm.w(r.i), &w_map, k * kBlockK, g.row_tile * kRows, sm.w_full(r.i), pol);
+                    else
+                        ptx::bulk_g2s(sm.w(r.i), src + (size_t)k * C::kWBytes, C::kWBytes, sm.w_full(r.i), pol);
+                    r.step(C::kWStages);
+                    ++issued;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---- x producer
+        if (lane == 0) {
+            bool ok = true;
+            const uint64_t pol = TN <= 32 ? ptx::policy_evict_last() : ptx::policy_evict_normal();
+            if (C::kInt8) ptx::pdl_wait_prior_grid();
+            while (ok && walk.next(g)) {
+                const int boxes = (g.n + C::kBox - 1) / C::kBox;
+                for (int k = g.k0 * C::kXPerBlock; k < g.k1 * C::kXPerBlock; ++k) {
+                    if (!wait(sm.x_empty(r.i), r.phase ^ 1, &s.abort, kErrRing)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::mbar_arrive_expect_tx(sm.x_full(r.i), boxes * C::kBox * 128);
+                    for (int b = 0; b < boxes; ++b)
+                        ptx::tma_load_2d(sm.x(r.i) + b * C::kBox * 128, &x_map, k * (kBlockK / C::kXPerBlock),
+                                         g.t0 + b * C::kBox, sm.x_full(r.i), pol);
+                    r.step(C::kXStages);
+                    ++issued;
+                }
+            }
+        }
+    } else if (warp == 2) {
+        // ---- MMA: one thread issues
+        if (lane == 0) {
+            Ring xr, wr, ar, dr;
+            bool ok = true;
+            while (ok && walk.next(g)) {
+                ok = wait(sm.d_empty(dr.i), dr.phase ^ 1, &s.abort, kErrAccumulator);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const int n16 = (g.n + 15) & ~15;
+                const uint32_t d = tmem + dr.i * TN;
+                const uint32_t idesc = C::kInt8 ? ptx::idesc_s8(n16) : ptx::idesc_f16(n16);
+                for (int k = g.k0; ok && k < g.k1; ++k) {
+                    if constexpr (C::kInt8) {
+                        ok = wait(sm.w_full(wr.i), wr.phase, &s.abort, kErrRing) &&
+                             wait(sm.x_full(xr.i), xr.phase, &s.abort, kErrRing);
+                        if (!ok) break;
+                        const uint64_t a = ptx::smem_desc_sw128(ptx::smem_addr(sm.w(wr.i)));
+                        const uint64_t b = ptx::smem_desc_sw128(ptx::smem_addr(sm.x(xr.i)));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            ptx::mma_s8_ss(d, a + 2 * j, b + 2 * j, idesc, k > g.k0 || j > 0);
+                        ptx::tc_commit(sm.w_empty(wr.i));
+                        ptx::tc_commit(sm.x_empty(xr.i));
+                        wr.step(C::kWStages);
+                        xr.step(C::kXStages);
+                    } else {
+                        ok = wait(sm.a_full(ar.i), ar.phase, &s.abort, kErrRing);
+                        if (!ok) break;
+                        const uint32_t a = tmem + C::kACol + ar.i * 64;
+                        for (int h = 0; h < 2; ++h) {
+                            ok = wait(sm.x_full(xr.i), xr.phase, &s.abort, kErrRing);
+                            if (!ok) break;
+                            ptx::tc_fence_after();
+                            const uint64_t b = ptx::smem_desc_sw128(ptx::smem_addr(sm.x(xr.i)));
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                ptx::mma_f16_ts(d, a + 32 * h + 8 * j, b + 2 * j, idesc, k > g.k0 || h > 0 || j > 0);
+                            ptx::tc_commit(sm.x_empty(xr.i));
+                            xr.step(C::kXStages);
+                        }
+                        if (!ok) break;
+                        ptx::tc_commit(sm.a_empty(ar.i));
+                        ar.step(C::kAStages);
+                    }
+                }
+                if (!ok) break;
+                ptx::tc_commit(sm.d_full(dr.i));
+                dr.step(C::kDStages);
+            }
+        }
+    } else if (warp >= 4 && warp < 4 + C::kDecodeWarps) {
+        // ---- decoders: thread = weight row (warp % 4, lane), half of the block's columns
+        if constexpr (!C::kInt8) {
+            Ring wr, ar;
+            const int row = (warp & 3) * 32 + lane, half = (warp - 4) >> 2;
+            const uint32_t dst = tmem + ((uint32_t)(warp & 3) << 21) + C::kACol + half * 32;
+            bool ok = true;
+            while (ok && walk.next(g)) {
+                for (int k = g.k0; k < g.k1; ++k) {
+                    ok = wait(sm.w_full(wr.i), wr.phase, &s.abort, kErrRing);
+                    if (!__all_sync(~0u, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t src = ptx::smem_addr(sm.w(wr.i));
+                    uint32_t h[32];
+                    if constexpr (FMT == SKINNY_FMT_NVFP4) {
+                        const uint4 c0 = ptx::lds128(src + (half * 2 * kRows + row) * 16);
+                        const uint4 c1 = ptx::lds128(src + (half * 2 * kRows + kRows + row) * 16);
+                        uint32_t sc;
+                        asm volatile("ld.shared.u32 %0, [%1];"
+                                     : "=r"(sc)
+                                     : "r"(src + kNvfp4BlockScales + (half * kRows + row) * 4)
+                                     : "memory");
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(sm.w_empty(wr.i));
+                        const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                        uint32_t s01, s23;
+                        ptx::e4m3x4_to_f16x4(sc, s01, s23);
+                        const uint32_t sd[4] = {ptx::dup_lo(s01), ptx::dup_hi(s01), ptx::dup_lo(s23),
+                                                ptx::dup_hi(s23)};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            uint32_t v[4];
+                            ptx::e2m1x8_to_f16x8(words[i], v);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) h[4 * i + j] = ptx::hmul2(v[j], sd[i / 2]);
+                        }
+                    } else {
+                        uint4 c[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) c[i] = ptx::lds128(src + ((half * 4 + i) * kRows + row) * 16);
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(sm.w_empty(wr.i));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            ptx::e4m3x4_to_f16x4(c[i].x, h[8 * i], h[8 * i + 1]);
+                            ptx::e4m3x4_to_f16x4(c[i].y, h[8 * i + 2], h[8 * i + 3]);
+                            ptx::e4m3x4_to_f16x4(c[i].z, h[8 * i + 4], h[8 * i + 5]);
+                            ptx::e4m3x4_to_f16x4(c[i].w, h[8 * i + 6], h[8 * i + 7]);
+                        }
+                    }
+                    wr.step(C::kWStages);
+                    ok = wait(sm.a_empty(ar.i), ar.phase ^ 1, &s.abort, kErrRing);
+                    if (!__all_sync(~0u, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    ptx::tmem_st32(dst + ar.i * 64, h);
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(sm.a_full(ar.i));
+                    ar.step(C::kAStages);
+                }
+            }
+        }
+    } else if (warp >= 4 + C::kDecodeWarps) {
+        // ---- epilogue: thread = output channel (warp % 4, lane)
+        Ring dr;
+        const int q = warp & 3, row = q * 32 + lane;
+        const uint32_t src = tmem + ((uint32_t)q << 21);
+        bool ok = true;
+        if (C::kInt8) ptx::pdl_wait_prior_grid();
+        while (ok && walk.next(g)) {
+            ok = wait(sm.d_full(dr.i), dr.phase, &s.abort, kErrAccumulator);
+            if (!__all_sync(~0u, ok)) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            const bool publish = g.k1 < p.C;
+            int lowest = blockIdx.x;     // first CTA whose partial sums belong to this tile
+            if (!publish && g.k0 > 0) {
+                const int64_t first = (int64_t)g.tile * p.C;
+                while (lowest > 0 && Walk<TN>::start(s, p, lowest) > first) --lowest;
+                // every thread waits for every flag itself: no thread reads a slot it has not acquired
+                const uint64_t t0 = ptx::globaltimer_ns();
+                for (int c = blockIdx.x - 1; ok && c >= lowest; --c) {
+                    if (Walk<TN>::start(s, p, c) == Walk<TN>::start(s, p, c + 1)) continue;
+                    while ((ptx::ld_acquire_gpu(p.flags + c) & kPublishedMask) != 4) {
+                        if (*(volatile int*)&s.abort) ok = false;
+                        else if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+                            s.abort = 1;
+                            atomicOr(&g_tile_error, kErrPartial);
+                            ok = false;
+                        }
+                        if (!ok) break;
+                    }
+                }
+                if (!__all_sync(~0u, ok)) {
+                    ok = false;
+                    break;
+                }
+            }
+            // This thread's channel and scale.  SiLU*mul tiles hold 16 gate
+            // rows and their 16 up rows in the two halves of every warp.
+            const int o = SILU ? g.row_tile * 64 + q * 16 + (lane & 15) : g.row_tile * kRows + row;
+            const bool valid = o < p.outputs;
+            float scale = 0.f;
+            if (valid && !publish) {
+                if (FMT == SKINNY_FMT_NVFP4) scale = p.scale[g.e];
+                else if (FMT == SKINNY_FMT_FP8)
+                    scale = p.scale[(size_t)g.e * p.N + o + (SILU && lane >= 16 ? p.outputs : 0)];
+                else scale = p.scale[o];
+            }
+            for (int c0 = 0; c0 < g.n; c0 += 32) {
+                uint32_t v[32];
+                ptx::tmem_ld32(src + dr.i * TN + c0, v);
+                if (publish) {
+                    unsigned* slot = p.partials + (size_t)blockIdx.x * kSlotWords + row;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c0 + j < g.n) slot[(c0 + j) * kRows] = v[j];
+                    continue;
+                }
+                for (int c = blockIdx.x - 1; c >= lowest; --c) {
+                    if (Walk<TN>::start(s, p, c) == Walk<TN>::start(s, p, c + 1)) continue;
+                    const unsigned* slot = p.partials + (size_t)c * kSlotWords + row;
+                    uint32_t o32[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o32[j] = c0 + j < g.n ? __ldcg(slot + (c0 + j) * kRows) : 0;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = C::kInt8 ? v[j] + o32[j]
+                                        : __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(o32[j]));
+                }
+                if constexpr (SILU) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        // lanes 0..15 finish token j, lanes 16..31 token j + 1
+                        const float a = __uint_as_float(v[j]) * scale, b = __uint_as_float(v[j + 1]) * scale;
+                        const float other = __shfl_xor_sync(~0u, lane < 16 ? b : a, 16);
+                        const float gate = lane < 16 ? a : other, up = lane < 16 ? other : b;
+                        const int t = c0 + j + (lane >> 4);
+                        if (valid && t < g.n)
+                            store_out(p.y, (int64_t)(g.t0 + t) * p.outputs + o, gate / (1.f + expf(-gate)) * up,
+                                      p.out_f32);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int t = c0 + j;
+                        if (valid && t < g.n) {
+                            const float r = C::kInt8 ? (float)(int)v[j] * p.row_scale[g.t0 + t] * scale
+                                                     : __uint_as_float(v[j]) * scale;
+                            store_out(p.y, (int64_t)(g.t0 + t) * p.outputs + o, r, p.out_f32);
+                        }
+                    }
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(sm.d_empty(dr.i));
+            dr.step(C::kDStages);
+            if (publish) {
+                if (lane == 0) ptx::atomic_add_release_gpu(p.flags + blockIdx.x, 1);
+            } else if (lane == 0) {
+                // The fourth warp to have read a slot frees it for the next call.
+                for (int c = blockIdx.x - 1; c >= lowest; --c) {
+                    if (Walk<TN>::start(s, p, c) == Walk<TN>::start(s, p, c + 1)) continue;
+                    if (atomicAdd(p.flags + c, kRead) == 4 + 3 * kRead) p.flags[c] = 0;
+                }
+            }
+        }
+    }
+
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (s.abort && lane == 0) {
+        // A wait gave up: copies and matrix instructions may still be in
+        // flight.  Let them end before the memory they use is given up.
+        if (warp == 0) drain(r, issued, C::kWStages, sm.w_full(0));
+        if (warp == 1) drain(r, issued, C::kXStages, sm.x_full(0));
+        if (warp == 2) {
+            ptx::tc_commit(sm.drained());
+            ptx::mbar_wait(sm.drained(), 0, kWaitLimitNs);
+        }
+    }
+    if (s.abort) __syncthreads();
+    if (warp == 2) ptx::tmem_free_all(tmem);
+}
+
+// Packs experts on the device: one thread per 16 bytes of a block's codes (or,
+// NVFP4, per row and half of its block scales).
+__global__ void pack_experts(int fmt, const uint8_t* codes, const uint8_t* scales, int N, int K, int outputs, int G,
+                             int Cb, int gate_up, uint8_t* packed)
+{
+    const int wb = block_bytes(fmt);
+    const int64_t blk = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;   // (e * G + g) * Cb + c
+    const int c = (int)(blk % Cb);
+    const int64_t eg = blk / Cb;
+    const int g = (int)(eg % G);
+    const int64_t e = eg / G;
+    uint8_t* out = packed + blk * wb;
+    const int row_bytes = fmt == SKINNY_FMT_NVFP4 ? K / 2 : K;
+    const int chunk_bytes = fmt == SKINNY_FMT_NVFP4 ? 64 : 128;
+    const int words = chunk_bytes / 16;
+    for (int i = threadIdx.x; i < kRows * (words + 1); i += blockDim.x) {
+        const int r = i % kRows, j = i / kRows;
+        const int l = r & 31;
+        const int o = gate_up ? g * 64 + (r / 32) * 16 + (l & 15) : g * kRows + r;
+        const int64_t n = o + (gate_up && l >= 16 ? outputs : 0);
+        if (j < words) {
+            for (int b = 0; b < 16; ++b) {
+                const int at = c * chunk_bytes + j * 16 + b;
+                out[(j * kRows + r) * 16 + b] =
+                    o < outputs && at < row_bytes ? codes[(e * N + n) * row_bytes + at] : 0;
+            }
+        } else if (fmt == SKINNY_FMT_NVFP4) {
+            for (int b = 0; b < 8; ++b) {
+                const int at = c * 8 + b;
+                out[kNvfp4BlockScales + ((b / 4) * kRows + r) * 4 + b % 4] =
+                    o < outputs && at < K / 16 ? scales[(e * N + n) * (K / 16) + at] : 0;
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+struct DeviceState {
+    bool ready = false;
+    int sms = 0;
+};
+std::mutex g_mu;
+DeviceState g_dev[kMaxDevices];
+EncodeTiled g_encode = nullptr;
+
+template <int FMT, int TN, bool SILU>
+bool allow_smem()
+{
+    return cudaFuncSetAttribute(tile_gemm<FMT, TN, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Cfg<FMT, TN>::kBytes) == cudaSuccess;
+}
+
+template <int FMT, bool SILU>
+bool allow_smem_all()
+{
+    return allow_smem<FMT, 32, SILU>() && allow_smem<FMT, 128, SILU>() && allow_smem<FMT, 256, SILU>();
+}
+
+// SM count of the current device; on its first use, the kernels' shared
+// memory limits and the tensor-map encoder.
+int current_device(int* sms)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SKINNY_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState& d = g_dev[dev];
+    if (!d.ready) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+            return SKINNY_ERR_CUDA;
+        if (!g_encode) {
+            void* fn = nullptr;
+            cudaDriverEntryPointQueryResult found;
+            if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
+                    cudaSuccess ||
+                found != cudaDriverEntryPointSuccess || !fn)
+                return SKINNY_ERR_CUDA;
+            g_encode = reinterpret_cast<EncodeTiled>(fn);
+        }
+        if (!allow_smem_all<SKINNY_FMT_NVFP4, false>() || !allow_smem_all<SKINNY_FMT_NVFP4, true>() ||
+            !allow_smem_all<SKINNY_FMT_FP8, false>() || !allow_smem_all<SKINNY_FMT_FP8, true>() ||
+            !allow_smem_all<kFmtInt8, false>())
+            return SKINNY_ERR_CUDA;
+        d.sms = n;
+        d.ready = true;
+    }
+    *sms = d.sms;
+    return SKINNY_OK;
+}
+
+// A row-major [rows][cols] matrix read in boxes of 128 bytes x box_rows rows.
+bool make_map(CUtensorMap* map, const void* base, bool f16, int64_t rows, int64_t cols, int box_rows)
+{
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)cols * (f16 ? 2 : 1)};
+    const cuuint32_t box[2] = {f16 ? 64u : 128u, (cuuint32_t)box_rows};
+    const cuuint32_t unit[2] = {1, 1};
+    return g_encode(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                    const_cast<void*>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t workspace_size(int sms) { return (size_t)sms * (kSlotWords + 1) * 4; }
+
+template <int FMT, int TN, bool SILU>
+int launch(Params p, const void* x, const void* w, int64_t K, int grid, cudaStream_t stream)
+{
+    using C = Cfg<FMT, TN>;
+    CUtensorMap xm, wm;
+    if (!make_map(&xm, x, !C::kInt8, p.T, K, C::kBox)) return SKINNY_ERR_CUDA;
+    if (C::kInt8) {
+        if (!make_map(&wm, w, false, p.N, K, kRows)) return SKINNY_ERR_CUDA;
+    } else {
+        wm = xm;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tile_gemm<FMT, TN, SILU>, p, xm, wm) == cudaSuccess ? SKINNY_OK : SKINNY_ERR_CUDA;
+}
+
+// Token columns per tile: `rows` is the number a tile would like to hold.
+// Narrow tiles leave the shared memory to the weights' ring (the memory-bound
+// range); wide ones reuse each decoded block more often.
+template <int FMT, bool SILU>
+int launch_any(const Params& p, const void* x, const void* w, int64_t K, int64_t rows, int grid, cudaStream_t stream)
+{
+    if (rows <= 32) return launch<FMT, 32, SILU>(p, x, w, K, grid, stream);
+    if (rows <= 128) return launch<FMT, 128, SILU>(p, x, w, K, grid, stream);
+    return launch<FMT, 256, SILU>(p, x, w, K, grid, stream);
+}
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+constexpr int64_t kMaxK = int64_t(1) << 20, kMaxN = int64_t(1) << 24, kMaxTokens = int64_t(1) << 24;
+
+int check_sizes(int64_t T, int64_t K, int64_t N)
+{
+    if (T < 0 || K <= 0 || K % 16 != 0 || N <= 0) return SKINNY_ERR_INVALID_ARG;
+    if (T > kMaxTokens || K > kMaxK || N > kMaxN) return SKINNY_ERR_UNSUPPORTED;
+    return SKINNY_OK;
+}
+
+// Fills in the workspace; `tiles` is the most tiles the launch can have.
+int set_workspace(Params* p, void* workspace, size_t bytes, int sms)
+{
+    p->partials = nullptr;
+    p->flags = nullptr;
+    if (!workspace) return SKINNY_OK;
+    if (bytes < workspace_size(sms)) return SKINNY_ERR_WORKSPACE;
+    p->partials = static_cast<unsigned*>(workspace);
+    p->flags = p->partials + (size_t)sms * kSlotWords;
+    return SKINNY_OK;
+}
+
+int experts(int fmt, const void* x, int64_t T, int64_t K, const int32_t* offsets, int64_t E, const void* w_packed,
+            const float* scale, int64_t N, bool silu, void* y, int out_dtype, void* workspace, size_t workspace_bytes,
+            void* stream)
+{
+    if (fmt != SKINNY_FMT_NVFP4 && fmt != SKINNY_FMT_FP8) return SKINNY_ERR_INVALID_ARG;
+    if (out_dtype != SKINNY_OUT_F16 && out_dtype != SKINNY_OUT_F32) return SKINNY_ERR_INVALID_ARG;
+    if (E <= 0 || (silu && N % 2 != 0)) return SKINNY_ERR_INVALID_ARG;
+    if (const int rc = check_sizes(T, K, N)) return rc;
+    if (E > kMaxExperts) return SKINNY_ERR_UNSUPPORTED;
+    if (T == 0) return SKINNY_OK;
+    if (!x || !offsets || !w_packed || !scale || !y) return SKINNY_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(w_packed, 16) || !aligned(offsets, 4) || !aligned(scale, 4) ||
+        !aligned(y, out_dtype == SKINNY_OUT_F32 ? 4 : 2) || (workspace && !aligned(workspace, 16)))
+        return SKINNY_ERR_ALIGNMENT;
+    Params p{};
+    p.w = static_cast<const uint8_t*>(w_packed);
+    p.scale = scale;
+    p.offsets = offsets;
+    p.y = y;
+    p.T = (int)T;
+    p.N = (int)N;
+    p.E = (int)E;
+    p.outputs = (int)(silu ? N / 2 : N);
+    p.G = (p.outputs + (silu ? 63 : kRows - 1)) / (silu ? 64 : kRows);
+    p.C = (int)((K + kBlockK - 1) / kBlockK);
+    p.out_f32 = out_dtype == SKINNY_OUT_F32;
+    // the running number of tiles is a 32-bit count
+    if ((T / 16 + E) * (int64_t)p.G >= (int64_t(1) << 31)) return SKINNY_ERR_UNSUPPORTED;
+    int sms = 0;
+    if (const int rc = current_device(&sms)) return rc;
+    if (const int rc = set_workspace(&p, workspace, workspace_bytes, sms)) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // Routers load experts unevenly: twice the mean.
+    const int64_t rows = T <= 32 ? T : 2 * ((T + E - 1) / E);
+    if (fmt == SKINNY_FMT_NVFP4)
+        return silu ? launch_any<SKINNY_FMT_NVFP4, true>(p, x, nullptr, K, rows, sms, st)
+                    : launch_any<SKINNY_FMT_NVFP4, false>(p, x, nullptr, K, rows, sms, st);
+    return silu ? launch_any<SKINNY_FMT_FP8, true>(p, x, nullptr, K, rows, sms, st)
+                : launch_any<SKINNY_FMT_FP8, false>(p, x, nullptr, K, rows, sms, st);
+}
+
+bool experts_shape(int fmt, int64_t E, int64_t N, int64_t K, int gate_up, int64_t* G, int64_t* C)
+{
+    if (fmt != SKINNY_FMT_NVFP4 && fmt != SKINNY_FMT_FP8) return false;
+    if (E <= 0 || E > kMaxExperts || N <= 0 || N > kMaxN || K <= 0 || K > kMaxK || K % 16 != 0) return false;
+    if (gate_up && N % 2 != 0) return false;
+    *G = gate_up ? (N / 2 + 63) / 64 : (N + kRows - 1) / kRows;
+    *C = (K + kBlockK - 1) / kBlockK;
+    return true;
+}
+
+}  // namespace
+}  // namespace skinny
+
+using namespace skinny;
+
+extern "C" size_t skinny_experts_packed_bytes(int fmt, int64_t E, int64_t N, int64_t K, int gate_up)
+{
+    int64_t G, C;
+    return experts_shape(fmt, E, N, K, gate_up, &G, &C) ? (size_t)(E * G * C) * block_bytes(fmt) : 0;
+}
+
+extern "C" int skinny_pack_experts(int fmt, const void* codes, const void* scales, int64_t E, int64_t N, int64_t K,
+                                   int gate_up, void* w_packed, void* stream)
+{
+    int64_t G, C;
+    if (!experts_shape(fmt, E, N, K, gate_up, &G, &C)) return SKINNY_ERR_INVALID_ARG;
+    if (!codes || !w_packed || (fmt == SKINNY_FMT_NVFP4 && !scales)) return SKINNY_ERR_INVALID_ARG;
+    if (!aligned(w_packed, 16)) return SKINNY_ERR_ALIGNMENT;
+    if (E * G >= 65536 * int64_t(1024)) return SKINNY_ERR_UNSUPPORTED;
+    // block index = x + y * gridDim.x over exactly E * G * C blocks
+    int64_t gx = E * G * C, gy = 1;
+    if (gx >= (int64_t(1) << 31)) {
+        gx = E * G;
+        gy = C;
+    }
+    pack_experts<<<dim3((unsigned)gx, (unsigned)gy), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+        fmt, static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), (int)N, (int)K,
+        (int)(gate_up ? N / 2 : N), (int)G, (int)C, gate_up, static_cast<uint8_t*>(w_packed));
+    return cudaGetLastError() == cudaSuccess ? SKINNY_OK : SKINNY_ERR_CUDA;
+}
+
+extern "C" int skinny_tile_workspace_bytes(size_t* bytes)
+{
+    if (!bytes) return SKINNY_ERR_INVALID_ARG;
+    int sms = 0;
+    if (const int rc = current_device(&sms)) return rc;
+    *bytes = workspace_size(sms);
+    return SKINNY_OK;
+}
+
+extern "C" int skinny_gemm_experts(int fmt, const void* x, int64_t T, int64_t K, const int32_t* offsets, int64_t E,
+                                   const void* w_packed, const float* scale, int64_t N, void* y, int out_dtype,
+                                   void* workspace, size_t workspace_bytes, void* stream)
+{
+    return experts(fmt, x, T, K, offsets, E, w_packed, scale, N, false, y, out_dtype, workspace, workspace_bytes,
+                   stream);
+}
+
+extern "C" int skinny_gemm_experts_silu_mul(int fmt, const void* x, int64_t T, int64_t K, const int32_t* offsets,
+                                            int64_t E, const void* w_packed, const float* scale, int64_t F, void* y,
+                                            int out_dtype, void* workspace, size_t workspace_bytes, void* stream)
+{
+    if (F <= 0 || F > kMaxN / 2) return SKINNY_ERR_INVALID_ARG;
+    return experts(fmt, x, T, K, offsets, E, w_packed, scale, 2 * F, true, y, out_dtype, workspace, workspace_bytes,
+                   stream);
+}
+
+extern "C" int skinny_int8_gemm(const void* q, const float* row_scale, int64_t M, int64_t K, const void* w,
+                                const float* channel_scale, int64_t N, void* y, int out_dtype, void* workspace,
+                                size_t workspace_bytes, void* stream)
+{
+    if (out_dtype != SKINNY_OUT_F16 && out_dtype != SKINNY_OUT_F32) return SKINNY_ERR_INVALID_ARG;
+    if (const int rc = check_sizes(M, K, N)) return rc;
+    if (K > SKINNY_MAX_INT8_K) return SKINNY_ERR_UNSUPPORTED;
+    if (M == 0) return SKINNY_OK;
+    if (!q || !row_scale || !w || !channel_scale || !y) return SKINNY_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(w, 16) || !aligned(row_scale, 4) || !aligned(channel_scale, 4) ||
+        !aligned(y, out_dtype == SKINNY_OUT_F32 ? 4 : 2) || (workspace && !aligned(workspace, 16)))
+        return SKINNY_ERR_ALIGNMENT;
+    Params p{};
+    p.scale = channel_scale;
+    p.row_scale = row_scale;
+    p.y = y;
+    p.T = (int)M;
+    p.N = p.outputs = (int)N;
+    p.E = 1;
+    p.G = (int)((N + kRows - 1) / kRows);
+    p.C = (int)((K + kBlockK - 1) / kBlockK);
+    p.out_f32 = out_dtype == SKINNY_OUT_F32;
+    if ((M / 16 + 1) * (int64_t)p.G >= (int64_t(1) << 31)) return SKINNY_ERR_UNSUPPORTED;
+    int sms = 0;
+    if (const int rc = current_device(&sms)) return rc;
+    if (const int rc = set_workspace(&p, workspace, workspace_bytes, sms)) return rc;
+    return launch_any<kFmtInt8, false>(p, q, w, K, M, sms, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int skinny_tile_device_error(int clear, unsigned* flags)
+{
+    if (!flags) return SKINNY_ERR_INVALID_ARG;
+    if (cudaDeviceSynchronize() != cudaSuccess) return SKINNY_ERR_CUDA;
+    unsigned v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_tile_error, sizeof(v)) != cudaSuccess) return SKINNY_ERR_CUDA;
+    *flags = v;
+    if (clear) {
+        const unsigned zero = 0;
+        if (cudaMemcpyToSymbol(g_tile_error, &zero, sizeof(zero)) != cudaSuccess) return SKINNY_ERR_CUDA;
+    }
+    return SKINNY_OK;
+}

@@ -329,6 +329,149 @@ size_t skinny_static_workspace_capacity(void);
 int skinny_debug_static_workspace_address(void** addr);
 
 /* ------------------------------------------------------------------------
+ * Products for any number of tokens: experts and 8-bit integers.
+ *
+ * These calls take any number of rows, from one to SKINNY_MAX_TOKENS, and run
+ * on the tcgen05 tensor cores.  Conventions as above (asynchronous on
+ * `stream`, caller-owned buffers, programmatic dependent launch), and:
+ *   - T = 0 (M = 0) returns SKINNY_OK and does nothing.
+ *   - The workspace (device, 16-byte aligned) is optional, has
+ *     skinny_tile_workspace_bytes() bytes on every shape, and must be
+ *     ZERO-filled before its first use; every call that completes without a
+ *     device error leaves its flags zero again.  It lets few tiles be split
+ *     along K over all SMs.  It must not be shared by calls that can run at
+ *     the same time, and the residency note of skinny_workspace_bytes applies.
+ *   - Sums are FP32 (int8: exact 32-bit integers) in an order that depends on
+ *     the sizes, the device and (experts) the row counts only, so results are
+ *     bitwise reproducible.
+ *   - K is a multiple of 16, K <= 2^20, N <= 2^24; larger sizes and products
+ *     of sizes past the tile counter's 31 bits return SKINNY_ERR_UNSUPPORTED.
+ * ---------------------------------------------------------------------- */
+
+#define SKINNY_MAX_EXPERTS 512
+#define SKINNY_MAX_TOKENS (1 << 24)
+
+/* Most columns of an int8 product: K * 128 * 128 stays below 2^31. */
+#define SKINNY_MAX_INT8_K 131056
+
+/* Size of the workspace of the calls below on the current device (128 KB and
+ * one flag per SM).  SKINNY_OK, or INVALID_ARG (null bytes) / CUDA. */
+int skinny_tile_workspace_bytes(size_t* bytes);
+
+/* Bytes of E packed experts of N x K weights each, in format fmt (a
+ * skinny_format); 0 if fmt, E, N or K is out of range, K % 16 != 0, or gate_up
+ * and N is odd. */
+size_t skinny_experts_packed_bytes(int fmt, int64_t E, int64_t N, int64_t K, int gate_up);
+
+/* Packs experts ON THE DEVICE, once, when a model is loaded.
+ *   codes     device: NVFP4 [E][N][K/2] (low nibble = even k), FP8 [E][N][K] E4M3.
+ *   scales    device, NVFP4: [E][N][K/16] UE4M3; FP8: ignored.
+ *   gate_up   non-zero: rows 0..N/2-1 are gate and N/2..N-1 up, packed for
+ *             skinny_gemm_experts_silu_mul.
+ *   w_packed  device, skinny_experts_packed_bytes() bytes, 16-byte aligned.
+ * Bytes that are no finite value are packed as they are (a product with them
+ * is NaN); the Python binding refuses them.  Asynchronous on `stream`.
+ * Errors: INVALID_ARG (null pointer, bad size or format), ALIGNMENT,
+ * UNSUPPORTED, CUDA. */
+int skinny_pack_experts(int fmt, const void* codes, const void* scales, int64_t E, int64_t N, int64_t K, int gate_up,
+                        void* w_packed, void* stream);
+
+/* Products grouped by expert, with ragged row counts:
+ *   y[r][n] = scale * sum_k W_e[n][k] x[r][k]   for offsets[e] <= r < offsets[e+1].
+ *   x         device [T][K] FP16, 16-byte aligned: rows sorted by expert.
+ *   offsets   device int32[E+1], non-decreasing, within [0, T].  They are read
+ *             by the kernel, so a router on the device needs no copy to the
+ *             host.  An offset outside [0, T], or below one before it, counts
+ *             as the nearest allowed value.  Rows before offsets[0] and from
+ *             offsets[E] on are not read and their y is left as it was.
+ *   E         1..SKINNY_MAX_EXPERTS experts; any of them may have no rows.
+ *   w_packed  device, from skinny_pack_experts(gate_up = 0), 16-byte aligned.
+ *   scale     device: NVFP4 float[E], one per expert; FP8 float[E][N], one per
+ *             expert and output channel.
+ *   y         device [T][N], FP16 (RNE) or FP32 per out_dtype, aligned to its type.
+ * Errors: see skinny_status; UNSUPPORTED for E > SKINNY_MAX_EXPERTS. */
+int skinny_gemm_experts(int fmt, const void* x, int64_t T, int64_t K, const int32_t* offsets, int64_t E,
+                        const void* w_packed, const float* scale, int64_t N, void* y, int out_dtype, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* The experts' gate+up product fused with SiLU*mul (as skinny_nvfp4_gemm_silu_mul):
+ *   y[r][j] = silu(g) * u,  g and u the rows j and F + j of the expert's product.
+ *   w_packed  from skinny_pack_experts(N = 2F, gate_up != 0).
+ *   scale     NVFP4 float[E]; FP8 float[E][2F].
+ *   y         device [T][F].
+ * Other arguments and errors as skinny_gemm_experts; F may be any number. */
+int skinny_gemm_experts_silu_mul(int fmt, const void* x, int64_t T, int64_t K, const int32_t* offsets, int64_t E,
+                                 const void* w_packed, const float* scale, int64_t F, void* y, int out_dtype,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* Activations to 8-bit integers with one scale per token:
+ *   row_scale[m] = max_k |x[m][k]| / 127 (FP32, rounded to nearest),
+ *   q[m][k] = x[m][k] / row_scale[m] to the nearest whole number (of the exact
+ *             quotient, ties to even), within [-127, 127].
+ * A row of zeros has scale 0 and q 0.  A row that holds an infinity or a NaN
+ * has scale NaN and q 0, so that its products come out NaN.
+ *   x          device [M][K], FP16 or FP32 per in_dtype (a skinny_out_dtype), 16-byte aligned.
+ *   q          device int8 [M][K], 16-byte aligned.
+ *   row_scale  device float[M]. */
+int skinny_quantize_int8(const void* x, int in_dtype, int64_t M, int64_t K, void* q, float* row_scale, void* stream);
+
+/* Product of 8-bit integers with a scale per token and per output channel:
+ *   y[m][n] = (sum_k q[m][k] w[n][k]) * row_scale[m] * channel_scale[n]
+ * The sum is exact; it is rounded to FP32, multiplied by row_scale[m], then by
+ * channel_scale[n], and rounded to the output type.
+ *   q              device int8 [M][K], 16-byte aligned.
+ *   w              device int8 [N][K] as it is (no packing), 16-byte aligned;
+ *                  like packed weights it must not be written by the kernel
+ *                  launched just before.
+ *   row_scale      device float[M];  channel_scale  device float[N].
+ *   y              device [M][N], FP16 or FP32 per out_dtype, aligned to its type.
+ * UNSUPPORTED for K > SKINNY_MAX_INT8_K. */
+int skinny_int8_gemm(const void* q, const float* row_scale, int64_t M, int64_t K, const void* w,
+                     const float* channel_scale, int64_t N, void* y, int out_dtype, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Device-side error word of the calls of this section on the current device,
+ * as skinny_device_error (1 = a ring slot, 2 = an accumulator, 4 = another
+ * CTA's partial sums).  After a call that set it, zero-fill the workspace. */
+int skinny_tile_device_error(int clear, unsigned* flags);
+
+/* ------------------------------------------------------------------------
+ * Verification of drafted tokens.
+ * ---------------------------------------------------------------------- */
+
+typedef enum { SKINNY_PROB_F16 = 0, SKINNY_PROB_F32 = 1, SKINNY_PROB_BF16 = 2 } skinny_prob_dtype;
+
+/* A verify round against the target's probabilities, from given random
+ * numbers (the sampled counterpart of skinny_nvfp4_gemm_argmax).  For each of
+ * B requests with up to S drafted tokens:
+ *   draft i is accepted if uniform[i] * q_i(d_i) < p_i(d_i), until one is not;
+ *   the next token is then drawn: at a draft that was not accepted from
+ *   max(p_i - q_i, 0), after the last accepted draft from p's next row, as the
+ *   first token v with a positive weight whose running sum w_0 + .. + w_v
+ *   exceeds uniform[S] times the whole sum.
+ * Comparisons and sums are made in 64 bits.
+ *   target        device [B][S+1][V] probabilities, unit stride along V and
+ *                 strides target_b, target_s (in elements); they need not sum to 1.
+ *   draft         device [B][S][V] likewise, or NULL for drafts without a
+ *                 distribution (found by lookup): q is then 1 at the draft.
+ *   prob_dtype    a skinny_prob_dtype, of target and draft.
+ *   draft_tokens  device int32 [B][S]; a token outside [0, V) is never accepted.
+ *   uniform       device float [B][S+1] in [0, 1): S for the drafts, then one
+ *                 for the draw.
+ *   num_drafts    device int32 [B], the drafts of each request (values outside
+ *                 [0, S] count as the nearest), or NULL for S each.
+ *   tokens        device int32 [B][S+1]: the accepted drafts, the drawn token, then -1.
+ *   accepted      device int32 [B]: how many drafts were accepted.
+ * Weights that are not finite count as 0.  Where max(p - q, 0) has no positive
+ * weight, the draw is from p; where p has none either, the token is -1.
+ * S = 0 draws one token from each target row.
+ * Errors: INVALID_ARG, ALIGNMENT; UNSUPPORTED for B > 2^20, S > 1024 or V > 2^28. */
+int skinny_verify_draft(const void* target, int64_t target_b, int64_t target_s, const void* draft, int64_t draft_b,
+                        int64_t draft_s, int prob_dtype, const int32_t* draft_tokens, const float* uniform,
+                        const int32_t* num_drafts, int64_t B, int64_t S, int64_t V, int32_t* tokens, int32_t* accepted,
+                        void* stream);
+
+/* ------------------------------------------------------------------------
  * Measurement.
  * ---------------------------------------------------------------------- */
 
