@@ -58,10 +58,10 @@ __device__ unsigned int g_tile_error;
 // them.  Zero between calls.
 constexpr unsigned kPublishedMask = 0xFF, kRead = 0x100;
 
-// Bytes of one packed 128 x 128 block.  A decoder thread reads its 64 columns
-// as 16-byte words, 128 rows side by side (no bank conflicts):
-//   NVFP4  [half][2 words][128 rows][32 codes], then [half][128 rows][4 block scales]
-//   FP8    [half][4 words][128 rows][16 codes]
+// Bytes of one packed 128 x 128 block.  A decoder thread reads its row's 128
+// columns as 16-byte words, 128 rows side by side (no bank conflicts):
+//   NVFP4  [4 words][128 rows][32 codes], then [128 rows][8 block scales]
+//   FP8    [8 words][128 rows][16 codes]
 __host__ __device__ constexpr int block_bytes(int fmt) { return fmt == SKINNY_FMT_NVFP4 ? 9216 : 16384; }
 constexpr int kNvfp4BlockScales = 8192;
 
@@ -73,41 +73,57 @@ struct Params {
     void* y;                     // [T][outputs]
     unsigned* partials;          // workspace: [P][kSlotWords], then [P] flags (or null)
     unsigned* flags;
-    int T, N, E;
+    int T, N, K, E;
     int G, C;                    // row tiles, K blocks
     int outputs;                 // outputs per token: N, or N / 2 (SiLU*mul)
     int out_f32;
 };
 
+constexpr int at_most(int a, int b) { return a < b ? a : b; }
+
 template <int FMT, int TN>
 struct Cfg {
     static constexpr bool kInt8 = FMT == kFmtInt8;
-    static constexpr int kWBytes = block_bytes(FMT);
-    static constexpr int kXPerBlock = kInt8 ? 1 : 2;         // 128-byte wide token boxes per K block
-    static constexpr int kXBytes = TN * 128;
-    static constexpr int kBox = TN <= 32 ? 16 : TN / 4;      // tokens per TMA box
-    static constexpr int kAStages = kInt8 ? 0 : 4;           // decoded blocks in tensor memory, 64 columns each
-    static constexpr int kACol = 256;
-    // Accumulators: two when they fit next to the decoded blocks.
-    static constexpr int kDStages = (kInt8 || TN <= 128) ? 2 : 1;
-    static constexpr int kDecodeWarps = kInt8 ? 0 : 8;
+    // A TMA or bulk copy costs its issuing thread 100 to 200 ns whatever its
+    // size, and narrow tiles leave a block only ~200 ns, so their ring slots
+    // hold two blocks of weights (one copy) and of tokens (one copy).
+    static constexpr int kWBlocks = (kInt8 && TN > 64) ? 1 : 2;                 // blocks per weight slot
+    static constexpr int kChunksPerBlock = kInt8 ? 1 : 2;                       // 128-byte wide pieces of x per block
+    static constexpr int kXChunks = TN > 64 ? 1 : 2 * kChunksPerBlock;          // pieces per token slot
+    static constexpr bool kX3d = kXChunks > 1;
+    static constexpr int kSmallBox = TN / 4;                                    // tokens of the small box (TN > 64)
+    static constexpr int kXProducers = TN > 64 ? 2 : 1;
+    static constexpr int kWBytes = block_bytes(FMT) * kWBlocks;
+    static constexpr int kChunkBytes = TN * 128;
+    static constexpr int kXBytes = kChunkBytes * kXChunks;
+    // Tensor memory: two accumulators at columns 0 and TN, then the decoded
+    // blocks, 64 columns each, at the end.
+    static constexpr int kDStages = 2;
+    static constexpr int kAStages = kInt8 ? 0 : TN > 128 ? 2 : 4;
+    static constexpr int kACol = 512 - 64 * kAStages;
+    // Groups of four decoder warps, which take turns: while one group waits
+    // for its stores, the others convert.
+    static constexpr int kGroups = kInt8 ? 0 : 2;
+    static constexpr int kDecodeWarps = 4 * kGroups;
     static constexpr int kWarps = 4 + kDecodeWarps + 4;
     static constexpr int kThreads = kWarps * 32;
-    // Ring slots: the tokens' ring holds at least two K blocks, the weights'
-    // ring takes what is left.
+    // Ring slots: tokens for about as many blocks as weights; next to wide
+    // token slots the weights' ring stays short.
     static constexpr int kBudget = 218 * 1024;
-    static constexpr int kXStages = kInt8 ? (kBudget / (kXBytes + kWBytes) < 12 ? kBudget / (kXBytes + kWBytes) : 12)
-                                          : (TN <= 32 ? 16 : TN <= 128 ? 6 : 4);
-    static constexpr int kWFit = (kBudget - kXStages * kXBytes) / kWBytes;
-    static constexpr int kWStages = kInt8 ? kXStages : (kWFit < 16 ? kWFit : 16);
+    static constexpr int kXPerW = kWBlocks * kChunksPerBlock / kXChunks;        // token slots per weight slot
+    static constexpr int kWStages = !kInt8 && TN > 64 ? (FMT == SKINNY_FMT_NVFP4 ? 4 : 3)
+                                                      : at_most(kBudget / (kWBytes + kXPerW * kXBytes), 10);
+    static constexpr int kXStages = at_most((kBudget - kWStages * kWBytes) / kXBytes, 16);
     static constexpr int kXOff = 0;
     static constexpr int kWOff = kXStages * kXBytes;
     static constexpr int kBarOff = kWOff + kWStages * kWBytes;
     static constexpr int kBars = 2 * (kXStages + kWStages + kAStages + kDStages) + 1;
     static constexpr int kBytes = kBarOff + kBars * 8 + 1024;   // + alignment of the dynamic shared memory
     static_assert(kBytes + 8 * (kMaxExperts + 2) + 256 <= 232448, "shared memory per CTA");
-    static_assert(kDStages * TN <= kACol || kInt8, "accumulators and decoded blocks overlap");
-    static_assert(kDStages * TN <= 512 && kACol + 64 * kAStages <= 512, "tensor memory");
+    static_assert(kDStages * TN <= kACol, "accumulators and decoded blocks overlap");
+    static_assert(kAStages >= kGroups, "a decoder group fills one stage at a time");
+    static_assert(kXBytes % 1024 == 0 && kWBytes % 1024 == 0, "swizzled tiles start on 1024 bytes");
+    static_assert(kXStages >= 2 && kWStages >= 2, "rings");
 };
 
 // The tile sequence, from the experts' row counts: expert e has
@@ -144,43 +160,40 @@ struct Segment {
     int tile, k0, k1;
 };
 
-// The CTA's pieces.  Few tiles are split along K so that every CTA streams
-// the same number of blocks (contiguous ranges of the tile sequence's blocks,
-// walked backwards: the partial sums that other CTAs wait for come first);
-// many tiles are dealt out whole, one after another, so that the CTAs work
-// on neighbouring tiles and share their operands in L2.
+// The CTA's pieces.  Whole tiles are dealt out one after another, so that the
+// CTAs work on neighbouring tiles and share their operands in L2.  What would
+// leave CTAs idle in the last round is split along K instead: the first
+// `splits` tiles (all, if there are fewer than two per CTA; otherwise the
+// remainder and one round) are cut into equal contiguous ranges of blocks,
+// one per CTA, and the partial sums of a cut tile meet in the workspace.  A
+// range is walked backwards, so that the sums another CTA waits for come first.
 template <int TN>
 struct Walk {
     const Schedule& s;
     const Params& p;
-    bool split;
-    int u0, u;       // split: first block, and one past the next piece's last
-    int tile;        // whole tiles: the next one
+    int share, extra;   // split blocks: CTA b has share + (b < extra)
+    int u0, u;          // this CTA's first block, and one past the next piece's last
+    int tile;           // the next whole tile
 
-    __device__ static bool use_split(const Schedule& s, const Params& p)
-    {
-        // From eight tiles per CTA on, the last round's idle CTAs cost less
-        // than the exchange of partial sums.
-        return p.partials != nullptr && s.total < 8 * (int)gridDim.x;
-    }
-    __device__ static int start(const Schedule& s, const Params& p, int b)
-    {
-        return (int)((int64_t)b * s.total * p.C / (int)gridDim.x);
-    }
     __device__ Walk(const Schedule& s_, const Params& p_) : s(s_), p(p_)
     {
-        split = use_split(s, p);
-        if (split) {
-            u0 = start(s, p, blockIdx.x);
-            u = start(s, p, blockIdx.x + 1);
-        } else {
-            tile = blockIdx.x;
+        const int P = gridDim.x, b = blockIdx.x;
+        int splits = 0;
+        if (p.partials != nullptr) {
+            if (s.total < 2 * P) splits = s.total;
+            else if (const int rest = s.total % P; rest != 0) splits = rest + P;
         }
+        share = splits * p.C / P;
+        extra = splits * p.C % P;
+        u0 = start(b);
+        u = start(b + 1);
+        tile = splits + b;
     }
+    __device__ int start(int b) const { return b * share + (b < extra ? b : extra); }
+    __device__ bool empty(int b) const { return share == 0 && b >= extra; }
     __device__ bool next(Segment& g)
     {
-        if (split) {
-            if (u <= u0) return false;
+        if (u > u0) {
             g.tile = (u - 1) / p.C;
             g.k1 = u - g.tile * p.C;
             g.k0 = u0 > g.tile * p.C ? u0 - g.tile * p.C : 0;
@@ -219,12 +232,15 @@ struct Ring {
 
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned code)
 {
-    const uint64_t t0 = ptx::globaltimer_ns();
+    // the clock only after some tries: reading it costs more than a short wait
+    uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
         if (ptx::mbar_try_wait(bar, parity)) return true;
-        if ((i & 15u) == 0) {
+        if ((i & 31u) == 0) {
             if (*abort) return false;
-            if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+            const uint64_t now = ptx::globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs) {
                 *abort = 1;
                 atomicOr(&g_tile_error, code);
                 return false;
@@ -240,10 +256,12 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort,
     return wait_slow(bar, parity, abort, code);
 }
 
-// Waits for a ring's copies in flight (the last `issued`, at most one round).
-__device__ __noinline__ void drain(Ring r, int issued, int stages, uint64_t* full)
+// Waits for a producer's copies in flight: of the slots before position r,
+// at most one round, every one that it filled (it fills one in `stride`).
+__device__ __noinline__ void drain(Ring r, int issued, int stride, int stages, uint64_t* full)
 {
-    for (int k = issued < stages ? issued : stages; k > 0; --k) {
+    const int n = issued * stride < stages ? issued * stride : stages;
+    for (int k = n; k > 0; --k) {
         if (r.i == 0) {
             r.i = stages;
             r.phase ^= 1;
@@ -328,7 +346,8 @@ __device__ __forceinline__ void store_out(void* y, int64_t at, float v, int f32)
 template <int FMT, int TN, bool SILU>
 __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
     tile_gemm(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap x_map,
-              const __grid_constant__ CUtensorMap w_map)
+              const __grid_constant__ CUtensorMap x_map2, const __grid_constant__ CUtensorMap w_map,
+              const __grid_constant__ CUtensorMap w_map2)
 {
     using C = Cfg<FMT, TN>;
     extern __shared__ uint8_t smem_raw[];
@@ -343,10 +362,10 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         }
         for (int i = 0; i < C::kWStages; ++i) {
             ptx::mbar_init(sm.w_full(i), 1);
-            ptx::mbar_init(sm.w_empty(i), C::kInt8 ? 1 : C::kDecodeWarps);
+            ptx::mbar_init(sm.w_empty(i), C::kInt8 ? 1 : 4 * C::kWBlocks);
         }
         for (int i = 0; i < C::kAStages; ++i) {
-            ptx::mbar_init(sm.a_full(i), C::kDecodeWarps);
+            ptx::mbar_init(sm.a_full(i), 4);
             ptx::mbar_init(sm.a_empty(i), 1);
         }
         for (int i = 0; i < C::kDStages; ++i) {
@@ -356,6 +375,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         ptx::mbar_init(sm.drained(), 1);
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&x_map);
+        ptx::prefetch_tensormap(&x_map2);
         if (C::kInt8) ptx::prefetch_tensormap(&w_map);
         s.abort = 0;
     }
@@ -382,47 +402,88 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
     Segment g;
     Ring r;            // the producers' position and how much they have issued
     int issued = 0;
+    // The single-thread roles run under elect.sync, which tells the compiler
+    // that one thread is active: a matrix instruction of 16 columns then issues
+    // every 9 clocks, under `lane == 0` every 68 (measured on B200).
+    bool mine = false;
 
     if (warp == 0) {
         // ---- W producer
-        if (lane == 0) {
+        if (ptx::elect_one()) {
+            mine = true;
             bool ok = true;
             const uint64_t pol = TN <= 32 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
             while (ok && walk.next(g)) {
                 const uint8_t* src =
-                    C::kInt8 ? nullptr : p.w + ((size_t)g.e * p.G + g.row_tile) * p.C * C::kWBytes;
-                for (int k = g.k0; k < g.k1; ++k) {
+                    C::kInt8 ? nullptr : p.w + ((size_t)g.e * p.G + g.row_tile) * p.C * block_bytes(FMT);
+                for (int k = g.k0; k < g.k1; k += C::kWBlocks) {
                     if (!wait(sm.w_empty(r.i), r.phase ^ 1, &s.abort, kErrRing)) {
                         ok = false;
                         break;
                     }
-                    ptx::mbar_arrive_expect_tx(sm.w_full(r.i), C::kWBytes);
-                    if constexpr (C::kInt8)
-                        ptx::tma_load_2d(sm.w(r.i), &w_map, k * kBlockK, g.row_tile * kRows, sm.w_full(r.i), pol);
-                    else
-                        ptx::bulk_g2s(sm.w(r.i), src + (size_t)k * C::kWBytes, C::kWBytes, sm.w_full(r.i), pol);
+                    if constexpr (C::kInt8) {
+                        ptx::mbar_arrive_expect_tx(sm.w_full(r.i), C::kWBytes);
+                        if (C::kWBlocks == 2 && (k + 2) * kBlockK <= p.K) {
+                            ptx::tma_load_3d(sm.w(r.i), &w_map, 0, g.row_tile * kRows, k, sm.w_full(r.i), pol);
+                        } else {
+                            // plain boxes: past K they fill in zeros
+                            for (int b = 0; b < C::kWBlocks; ++b)
+                                ptx::tma_load_2d(sm.w(r.i) + b * block_bytes(FMT), C::kWBlocks == 2 ? &w_map2 : &w_map,
+                                                 (k + b) * kBlockK, g.row_tile * kRows, sm.w_full(r.i), pol);
+                        }
+                    } else {
+                        const uint32_t bytes = (k + 1 < g.k1 ? 2 : 1) * block_bytes(FMT);
+                        ptx::mbar_arrive_expect_tx(sm.w_full(r.i), bytes);
+                        ptx::bulk_g2s(sm.w(r.i), src + (size_t)k * block_bytes(FMT), bytes, sm.w_full(r.i), pol);
+                    }
                     r.step(C::kWStages);
                     ++issued;
                 }
             }
         }
-    } else if (warp == 1) {
-        // ---- x producer
-        if (lane == 0) {
+    } else if (warp == 1 || (warp == 3 && C::kXProducers == 2)) {
+        // ---- x producers: two take turns where the slots are small for their time
+        if (ptx::elect_one()) {
+            mine = true;
             bool ok = true;
             const uint64_t pol = TN <= 32 ? ptx::policy_evict_last() : ptx::policy_evict_normal();
             if (C::kInt8) ptx::pdl_wait_prior_grid();
+            int turn = warp == 1 ? 0 : 1;
+            constexpr int kChunkK = kBlockK / C::kChunksPerBlock;
+            const int whole = p.K / kChunkK;      // pieces that lie within K entirely
             while (ok && walk.next(g)) {
-                const int boxes = (g.n + C::kBox - 1) / C::kBox;
-                for (int k = g.k0 * C::kXPerBlock; k < g.k1 * C::kXPerBlock; ++k) {
+                const int c1 = g.k1 * C::kChunksPerBlock;
+                for (int c = g.k0 * C::kChunksPerBlock; c < c1; c += C::kXChunks) {
+                    if (C::kXProducers == 2 && (turn ^= 1) == 0) {
+                        r.step(C::kXStages);
+                        continue;
+                    }
                     if (!wait(sm.x_empty(r.i), r.phase ^ 1, &s.abort, kErrRing)) {
                         ok = false;
                         break;
                     }
-                    ptx::mbar_arrive_expect_tx(sm.x_full(r.i), boxes * C::kBox * 128);
-                    for (int b = 0; b < boxes; ++b)
-                        ptx::tma_load_2d(sm.x(r.i) + b * C::kBox * 128, &x_map, k * (kBlockK / C::kXPerBlock),
-                                         g.t0 + b * C::kBox, sm.x_full(r.i), pol);
+                    if constexpr (C::kX3d) {
+                        // one box of kXChunks pieces; where K ends inside one, a box for each
+                        // piece, which fills in zeros past K
+                        ptx::mbar_arrive_expect_tx(sm.x_full(r.i), C::kXBytes);
+                        const int last = c + C::kXChunks < c1 ? c + C::kXChunks : c1;
+                        if (last <= whole) {
+                            ptx::tma_load_3d(sm.x(r.i), &x_map, 0, g.t0, c, sm.x_full(r.i), pol);
+                        } else {
+                            for (int b = 0; b < C::kXChunks; ++b)
+                                ptx::tma_load_2d(sm.x(r.i) + b * C::kChunkBytes, &x_map2, (c + b) * kChunkK, g.t0,
+                                                 sm.x_full(r.i), pol);
+                        }
+                    } else if (g.n > 2 * C::kSmallBox) {
+                        ptx::mbar_arrive_expect_tx(sm.x_full(r.i), C::kXBytes);
+                        ptx::tma_load_2d(sm.x(r.i), &x_map, c * kChunkK, g.t0, sm.x_full(r.i), pol);
+                    } else {
+                        const int boxes = g.n > C::kSmallBox ? 2 : 1;
+                        ptx::mbar_arrive_expect_tx(sm.x_full(r.i), boxes * C::kSmallBox * 128);
+                        for (int b = 0; b < boxes; ++b)
+                            ptx::tma_load_2d(sm.x(r.i) + b * C::kSmallBox * 128, &x_map2, c * kChunkK,
+                                             g.t0 + b * C::kSmallBox, sm.x_full(r.i), pol);
+                    }
                     r.step(C::kXStages);
                     ++issued;
                 }
@@ -430,7 +491,8 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         }
     } else if (warp == 2) {
         // ---- MMA: one thread issues
-        if (lane == 0) {
+        if (ptx::elect_one()) {
+            mine = true;
             Ring xr, wr, ar, dr;
             bool ok = true;
             while (ok && walk.next(g)) {
@@ -440,36 +502,47 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                 const int n16 = (g.n + 15) & ~15;
                 const uint32_t d = tmem + dr.i * TN;
                 const uint32_t idesc = C::kInt8 ? ptx::idesc_s8(n16) : ptx::idesc_f16(n16);
+                int xc = 0;      // piece within the token slot
                 for (int k = g.k0; ok && k < g.k1; ++k) {
+                    const int wb = (k - g.k0) % C::kWBlocks;
+                    const bool last = k + 1 == g.k1;
                     if constexpr (C::kInt8) {
-                        ok = wait(sm.w_full(wr.i), wr.phase, &s.abort, kErrRing) &&
-                             wait(sm.x_full(xr.i), xr.phase, &s.abort, kErrRing);
-                        if (!ok) break;
-                        const uint64_t a = ptx::smem_desc_sw128(ptx::smem_addr(sm.w(wr.i)));
-                        const uint64_t b = ptx::smem_desc_sw128(ptx::smem_addr(sm.x(xr.i)));
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            ptx::mma_s8_ss(d, a + 2 * j, b + 2 * j, idesc, k > g.k0 || j > 0);
-                        ptx::tc_commit(sm.w_empty(wr.i));
-                        ptx::tc_commit(sm.x_empty(xr.i));
-                        wr.step(C::kWStages);
-                        xr.step(C::kXStages);
+                        if (wb == 0) ok = wait(sm.w_full(wr.i), wr.phase, &s.abort, kErrRing);
                     } else {
                         ok = wait(sm.a_full(ar.i), ar.phase, &s.abort, kErrRing);
+                    }
+                    if (!ok) break;
+#pragma unroll
+                    for (int h = 0; h < C::kChunksPerBlock; ++h) {
+                        if (xc == 0) ok = wait(sm.x_full(xr.i), xr.phase, &s.abort, kErrRing);
                         if (!ok) break;
-                        const uint32_t a = tmem + C::kACol + ar.i * 64;
-                        for (int h = 0; h < 2; ++h) {
-                            ok = wait(sm.x_full(xr.i), xr.phase, &s.abort, kErrRing);
-                            if (!ok) break;
-                            ptx::tc_fence_after();
-                            const uint64_t b = ptx::smem_desc_sw128(ptx::smem_addr(sm.x(xr.i)));
+                        ptx::tc_fence_after();
+                        const uint64_t b = ptx::smem_desc_sw128(ptx::smem_addr(sm.x(xr.i) + xc * C::kChunkBytes));
+                        if constexpr (C::kInt8) {
+                            const uint64_t a =
+                                ptx::smem_desc_sw128(ptx::smem_addr(sm.w(wr.i) + wb * block_bytes(FMT)));
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                ptx::mma_s8_ss(d, a + 2 * j, b + 2 * j, idesc, k > g.k0 || j > 0);
+                        } else {
+                            const uint32_t a = tmem + C::kACol + ar.i * 64;
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
                                 ptx::mma_f16_ts(d, a + 32 * h + 8 * j, b + 2 * j, idesc, k > g.k0 || h > 0 || j > 0);
+                        }
+                        if (++xc == C::kXChunks || (last && h == C::kChunksPerBlock - 1)) {
                             ptx::tc_commit(sm.x_empty(xr.i));
                             xr.step(C::kXStages);
+                            xc = 0;
                         }
-                        if (!ok) break;
+                    }
+                    if (!ok) break;
+                    if constexpr (C::kInt8) {
+                        if (wb == C::kWBlocks - 1 || last) {
+                            ptx::tc_commit(sm.w_empty(wr.i));
+                            wr.step(C::kWStages);
+                        }
+                    } else {
                         ptx::tc_commit(sm.a_empty(ar.i));
                         ar.step(C::kAStages);
                     }
@@ -480,70 +553,78 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             }
         }
     } else if (warp >= 4 && warp < 4 + C::kDecodeWarps) {
-        // ---- decoders: thread = weight row (warp % 4, lane), half of the block's columns
+        // ---- decoders: thread = weight row (warp % 4, lane); the groups take blocks in turn
         if constexpr (!C::kInt8) {
             Ring wr, ar;
-            const int row = (warp & 3) * 32 + lane, half = (warp - 4) >> 2;
-            const uint32_t dst = tmem + ((uint32_t)(warp & 3) << 21) + C::kACol + half * 32;
+            const int row = (warp & 3) * 32 + lane;
+            int turn = (warp - 4) >> 2;      // blocks until this group's next
+            const uint32_t dst = tmem + ((uint32_t)(warp & 3) << 21) + C::kACol;
             bool ok = true;
             while (ok && walk.next(g)) {
                 for (int k = g.k0; k < g.k1; ++k) {
-                    ok = wait(sm.w_full(wr.i), wr.phase, &s.abort, kErrRing);
-                    if (!__all_sync(~0u, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t src = ptx::smem_addr(sm.w(wr.i));
-                    uint32_t h[32];
-                    if constexpr (FMT == SKINNY_FMT_NVFP4) {
-                        const uint4 c0 = ptx::lds128(src + (half * 2 * kRows + row) * 16);
-                        const uint4 c1 = ptx::lds128(src + (half * 2 * kRows + kRows + row) * 16);
-                        uint32_t sc;
-                        asm volatile("ld.shared.u32 %0, [%1];"
-                                     : "=r"(sc)
-                                     : "r"(src + kNvfp4BlockScales + (half * kRows + row) * 4)
-                                     : "memory");
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(sm.w_empty(wr.i));
-                        const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-                        uint32_t s01, s23;
-                        ptx::e4m3x4_to_f16x4(sc, s01, s23);
-                        const uint32_t sd[4] = {ptx::dup_lo(s01), ptx::dup_hi(s01), ptx::dup_lo(s23),
-                                                ptx::dup_hi(s23)};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            uint32_t v[4];
-                            ptx::e2m1x8_to_f16x8(words[i], v);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) h[4 * i + j] = ptx::hmul2(v[j], sd[i / 2]);
+                    const int wb = (k - g.k0) % C::kWBlocks;
+                    const bool alone = wb == 0 && k + 1 == g.k1;      // a slot with one block
+                    if (turn == 0) {
+                        turn = C::kGroups - 1;
+                        ok = wait(sm.w_full(wr.i), wr.phase, &s.abort, kErrRing);
+                        if (!__all_sync(~0u, ok)) {
+                            ok = false;
+                            break;
                         }
+                        const uint32_t src = ptx::smem_addr(sm.w(wr.i) + wb * block_bytes(FMT));
+                        constexpr int kWords = FMT == SKINNY_FMT_NVFP4 ? 4 : 8;
+                        uint4 c[kWords];
+#pragma unroll
+                        for (int i = 0; i < kWords; ++i) c[i] = ptx::lds128(src + (i * kRows + row) * 16);
+                        uint32_t sc[2] = {0, 0};
+                        if constexpr (FMT == SKINNY_FMT_NVFP4) ptx::lds64(src + kNvfp4BlockScales + row * 8, sc);
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive_n(sm.w_empty(wr.i), alone ? C::kWBlocks : 1);
+                        ok = wait(sm.a_empty(ar.i), ar.phase ^ 1, &s.abort, kErrRing);
+                        if (!__all_sync(~0u, ok)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t v[32];
+                            if constexpr (FMT == SKINNY_FMT_NVFP4) {
+                                uint32_t s01, s23;
+                                ptx::e4m3x4_to_f16x4(sc[h], s01, s23);
+                                const uint32_t sd[4] = {ptx::dup_lo(s01), ptx::dup_hi(s01), ptx::dup_lo(s23),
+                                                        ptx::dup_hi(s23)};
+                                const uint32_t words[8] = {c[2 * h].x,     c[2 * h].y,     c[2 * h].z,
+                                                           c[2 * h].w,     c[2 * h + 1].x, c[2 * h + 1].y,
+                                                           c[2 * h + 1].z, c[2 * h + 1].w};
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    uint32_t f[4];
+                                    ptx::e2m1x8_to_f16x8(words[i], f);
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j) v[4 * i + j] = ptx::hmul2(f[j], sd[i / 2]);
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint4 w = c[4 * h + i];
+                                    ptx::e4m3x4_to_f16x4(w.x, v[8 * i], v[8 * i + 1]);
+                                    ptx::e4m3x4_to_f16x4(w.y, v[8 * i + 2], v[8 * i + 3]);
+                                    ptx::e4m3x4_to_f16x4(w.z, v[8 * i + 4], v[8 * i + 5]);
+                                    ptx::e4m3x4_to_f16x4(w.w, v[8 * i + 6], v[8 * i + 7]);
+                                }
+                            }
+                            ptx::tmem_st32(dst + ar.i * 64 + h * 32, v);
+                        }
+                        ptx::tmem_wait_st();
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(sm.a_full(ar.i));
                     } else {
-                        uint4 c[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) c[i] = ptx::lds128(src + ((half * 4 + i) * kRows + row) * 16);
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(sm.w_empty(wr.i));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            ptx::e4m3x4_to_f16x4(c[i].x, h[8 * i], h[8 * i + 1]);
-                            ptx::e4m3x4_to_f16x4(c[i].y, h[8 * i + 2], h[8 * i + 3]);
-                            ptx::e4m3x4_to_f16x4(c[i].z, h[8 * i + 4], h[8 * i + 5]);
-                            ptx::e4m3x4_to_f16x4(c[i].w, h[8 * i + 6], h[8 * i + 7]);
-                        }
+                        --turn;
                     }
-                    wr.step(C::kWStages);
-                    ok = wait(sm.a_empty(ar.i), ar.phase ^ 1, &s.abort, kErrRing);
-                    if (!__all_sync(~0u, ok)) {
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after();
-                    ptx::tmem_st32(dst + ar.i * 64, h);
-                    ptx::tmem_wait_st();
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(sm.a_full(ar.i));
                     ar.step(C::kAStages);
+                    if (wb == C::kWBlocks - 1 || k + 1 == g.k1) wr.step(C::kWStages);
                 }
             }
         }
@@ -564,12 +645,12 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             const bool publish = g.k1 < p.C;
             int lowest = blockIdx.x;     // first CTA whose partial sums belong to this tile
             if (!publish && g.k0 > 0) {
-                const int64_t first = (int64_t)g.tile * p.C;
-                while (lowest > 0 && Walk<TN>::start(s, p, lowest) > first) --lowest;
+                const int first = g.tile * p.C;
+                while (lowest > 0 && walk.start(lowest) > first) --lowest;
                 // every thread waits for every flag itself: no thread reads a slot it has not acquired
                 const uint64_t t0 = ptx::globaltimer_ns();
                 for (int c = blockIdx.x - 1; ok && c >= lowest; --c) {
-                    if (Walk<TN>::start(s, p, c) == Walk<TN>::start(s, p, c + 1)) continue;
+                    if (walk.empty(c)) continue;
                     while ((ptx::ld_acquire_gpu(p.flags + c) & kPublishedMask) != 4) {
                         if (*(volatile int*)&s.abort) ok = false;
                         else if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
@@ -598,7 +679,14 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             }
             for (int c0 = 0; c0 < g.n; c0 += 32) {
                 uint32_t v[32];
-                ptx::tmem_ld32(src + dr.i * TN + c0, v);
+                if constexpr (TN == 16) {
+                    uint32_t lo[16];
+                    ptx::tmem_ld16(src + dr.i * TN + c0, lo);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = j < 16 ? lo[j] : 0;
+                } else {
+                    ptx::tmem_ld32(src + dr.i * TN + c0, v);
+                }
                 if (publish) {
                     unsigned* slot = p.partials + (size_t)blockIdx.x * kSlotWords + row;
 #pragma unroll
@@ -607,7 +695,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                     continue;
                 }
                 for (int c = blockIdx.x - 1; c >= lowest; --c) {
-                    if (Walk<TN>::start(s, p, c) == Walk<TN>::start(s, p, c + 1)) continue;
+                    if (walk.empty(c)) continue;
                     const unsigned* slot = p.partials + (size_t)c * kSlotWords + row;
                     uint32_t o32[32];
 #pragma unroll
@@ -650,7 +738,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             } else if (lane == 0) {
                 // The fourth warp to have read a slot frees it for the next call.
                 for (int c = blockIdx.x - 1; c >= lowest; --c) {
-                    if (Walk<TN>::start(s, p, c) == Walk<TN>::start(s, p, c + 1)) continue;
+                    if (walk.empty(c)) continue;
                     if (atomicAdd(p.flags + c, kRead) == 4 + 3 * kRead) p.flags[c] = 0;
                 }
             }
@@ -661,11 +749,11 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (s.abort && lane == 0) {
+    if (s.abort && mine) {
         // A wait gave up: copies and matrix instructions may still be in
         // flight.  Let them end before the memory they use is given up.
-        if (warp == 0) drain(r, issued, C::kWStages, sm.w_full(0));
-        if (warp == 1) drain(r, issued, C::kXStages, sm.x_full(0));
+        if (warp == 0) drain(r, issued, 1, C::kWStages, sm.w_full(0));
+        if (warp == 1 || (warp == 3 && C::kXProducers == 2)) drain(r, issued, C::kXProducers, C::kXStages, sm.x_full(0));
         if (warp == 2) {
             ptx::tc_commit(sm.drained());
             ptx::mbar_wait(sm.drained(), 0, kWaitLimitNs);
@@ -704,7 +792,7 @@ __global__ void pack_experts(int fmt, const uint8_t* codes, const uint8_t* scale
         } else if (fmt == SKINNY_FMT_NVFP4) {
             for (int b = 0; b < 8; ++b) {
                 const int at = c * 8 + b;
-                out[kNvfp4BlockScales + ((b / 4) * kRows + r) * 4 + b % 4] =
+                out[kNvfp4BlockScales + r * 8 + b] =
                     o < outputs && at < K / 16 ? scales[(e * N + n) * (K / 16) + at] : 0;
             }
         }
@@ -727,6 +815,11 @@ std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
 EncodeTiled g_encode = nullptr;
 
+// Widest token tile: two accumulators, and (experts) two decoded blocks, fill
+// the tensor memory.
+template <int FMT>
+constexpr int kWidest = FMT == kFmtInt8 ? 256 : 192;
+
 template <int FMT, int TN, bool SILU>
 bool allow_smem()
 {
@@ -737,7 +830,8 @@ bool allow_smem()
 template <int FMT, bool SILU>
 bool allow_smem_all()
 {
-    return allow_smem<FMT, 32, SILU>() && allow_smem<FMT, 128, SILU>() && allow_smem<FMT, 256, SILU>();
+    return allow_smem<FMT, 16, SILU>() && allow_smem<FMT, 32, SILU>() && allow_smem<FMT, 64, SILU>() &&
+           allow_smem<FMT, 128, SILU>() && allow_smem<FMT, kWidest<FMT>, SILU>();
 }
 
 // SM count of the current device; on its first use, the kernels' shared
@@ -772,14 +866,23 @@ int current_device(int* sms)
     return SKINNY_OK;
 }
 
-// A row-major [rows][cols] matrix read in boxes of 128 bytes x box_rows rows.
-bool make_map(CUtensorMap* map, const void* base, bool f16, int64_t rows, int64_t cols, int box_rows)
+// A row-major [rows][cols] matrix read in boxes of 128 bytes x box_rows rows,
+// or (pieces > 1) in boxes of `pieces` of these side by side in K, each a tile
+// of its own in shared memory: the matrix is then seen as [cols / 128 bytes]
+// pieces of rows, without the columns that fill no piece.
+bool make_map(CUtensorMap* map, const void* base, bool f16, int64_t rows, int64_t cols, int box_rows, int pieces)
 {
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)cols * (f16 ? 2 : 1)};
-    const cuuint32_t box[2] = {f16 ? 64u : 128u, (cuuint32_t)box_rows};
-    const cuuint32_t unit[2] = {1, 1};
-    return g_encode(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+    const cuuint64_t pitch = (cuuint64_t)cols * (f16 ? 2 : 1);
+    const cuuint32_t wide = f16 ? 64u : 128u;
+    const cuuint64_t whole = (cuuint64_t)cols / wide;
+    const bool split = pieces > 1;
+    // Fewer columns than one piece: no box of this kind is read.
+    if (split && whole == 0) return make_map(map, base, f16, rows, cols, box_rows, 1);
+    const cuuint64_t dims[3] = {split ? wide : (cuuint64_t)cols, (cuuint64_t)rows, whole};
+    const cuuint64_t strides[2] = {pitch, 128};
+    const cuuint32_t box[3] = {wide, (cuuint32_t)box_rows, (cuuint32_t)pieces};
+    const cuuint32_t unit[3] = {1, 1, 1};
+    return g_encode(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, split ? 3 : 2,
                     const_cast<void*>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -788,15 +891,16 @@ bool make_map(CUtensorMap* map, const void* base, bool f16, int64_t rows, int64_
 size_t workspace_size(int sms) { return (size_t)sms * (kSlotWords + 1) * 4; }
 
 template <int FMT, int TN, bool SILU>
-int launch(Params p, const void* x, const void* w, int64_t K, int grid, cudaStream_t stream)
+int launch(Params p, const void* x, const void* w, int grid, cudaStream_t stream)
 {
     using C = Cfg<FMT, TN>;
-    CUtensorMap xm, wm;
-    if (!make_map(&xm, x, !C::kInt8, p.T, K, C::kBox)) return SKINNY_ERR_CUDA;
+    CUtensorMap xm, xm2, wm, wm2;
+    if (!make_map(&xm, x, !C::kInt8, p.T, p.K, TN, C::kXChunks)) return SKINNY_ERR_CUDA;
+    if (!make_map(&xm2, x, !C::kInt8, p.T, p.K, C::kX3d ? TN : C::kSmallBox, 1)) return SKINNY_ERR_CUDA;
+    wm = wm2 = xm;
     if (C::kInt8) {
-        if (!make_map(&wm, w, false, p.N, K, kRows)) return SKINNY_ERR_CUDA;
-    } else {
-        wm = xm;
+        if (!make_map(&wm, w, false, p.N, p.K, kRows, C::kWBlocks)) return SKINNY_ERR_CUDA;
+        if (C::kWBlocks > 1 && !make_map(&wm2, w, false, p.N, p.K, kRows, 1)) return SKINNY_ERR_CUDA;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -808,18 +912,20 @@ int launch(Params p, const void* x, const void* w, int64_t K, int grid, cudaStre
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tile_gemm<FMT, TN, SILU>, p, xm, wm) == cudaSuccess ? SKINNY_OK : SKINNY_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, tile_gemm<FMT, TN, SILU>, p, xm, xm2, wm, wm2) == cudaSuccess ? SKINNY_OK : SKINNY_ERR_CUDA;
 }
 
 // Token columns per tile: `rows` is the number a tile would like to hold.
 // Narrow tiles leave the shared memory to the weights' ring (the memory-bound
 // range); wide ones reuse each decoded block more often.
 template <int FMT, bool SILU>
-int launch_any(const Params& p, const void* x, const void* w, int64_t K, int64_t rows, int grid, cudaStream_t stream)
+int launch_any(const Params& p, const void* x, const void* w, int64_t rows, int grid, cudaStream_t stream)
 {
-    if (rows <= 32) return launch<FMT, 32, SILU>(p, x, w, K, grid, stream);
-    if (rows <= 128) return launch<FMT, 128, SILU>(p, x, w, K, grid, stream);
-    return launch<FMT, 256, SILU>(p, x, w, K, grid, stream);
+    if (rows <= 16) return launch<FMT, 16, SILU>(p, x, w, grid, stream);
+    if (rows <= 32) return launch<FMT, 32, SILU>(p, x, w, grid, stream);
+    if (rows <= 64) return launch<FMT, 64, SILU>(p, x, w, grid, stream);
+    if (rows <= 128) return launch<FMT, 128, SILU>(p, x, w, grid, stream);
+    return launch<FMT, kWidest<FMT>, SILU>(p, x, w, grid, stream);
 }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -866,6 +972,7 @@ int experts(int fmt, const void* x, int64_t T, int64_t K, const int32_t* offsets
     p.y = y;
     p.T = (int)T;
     p.N = (int)N;
+    p.K = (int)K;
     p.E = (int)E;
     p.outputs = (int)(silu ? N / 2 : N);
     p.G = (p.outputs + (silu ? 63 : kRows - 1)) / (silu ? 64 : kRows);
@@ -880,10 +987,10 @@ int experts(int fmt, const void* x, int64_t T, int64_t K, const int32_t* offsets
     // Routers load experts unevenly: twice the mean.
     const int64_t rows = T <= 32 ? T : 2 * ((T + E - 1) / E);
     if (fmt == SKINNY_FMT_NVFP4)
-        return silu ? launch_any<SKINNY_FMT_NVFP4, true>(p, x, nullptr, K, rows, sms, st)
-                    : launch_any<SKINNY_FMT_NVFP4, false>(p, x, nullptr, K, rows, sms, st);
-    return silu ? launch_any<SKINNY_FMT_FP8, true>(p, x, nullptr, K, rows, sms, st)
-                : launch_any<SKINNY_FMT_FP8, false>(p, x, nullptr, K, rows, sms, st);
+        return silu ? launch_any<SKINNY_FMT_NVFP4, true>(p, x, nullptr, rows, sms, st)
+                    : launch_any<SKINNY_FMT_NVFP4, false>(p, x, nullptr, rows, sms, st);
+    return silu ? launch_any<SKINNY_FMT_FP8, true>(p, x, nullptr, rows, sms, st)
+                : launch_any<SKINNY_FMT_FP8, false>(p, x, nullptr, rows, sms, st);
 }
 
 bool experts_shape(int fmt, int64_t E, int64_t N, int64_t K, int gate_up, int64_t* G, int64_t* C)
@@ -971,6 +1078,7 @@ extern "C" int skinny_int8_gemm(const void* q, const float* row_scale, int64_t M
     p.y = y;
     p.T = (int)M;
     p.N = p.outputs = (int)N;
+    p.K = (int)K;
     p.E = 1;
     p.G = (int)((N + kRows - 1) / kRows);
     p.C = (int)((K + kBlockK - 1) / kBlockK);
@@ -979,7 +1087,7 @@ extern "C" int skinny_int8_gemm(const void* q, const float* row_scale, int64_t M
     int sms = 0;
     if (const int rc = current_device(&sms)) return rc;
     if (const int rc = set_workspace(&p, workspace, workspace_bytes, sms)) return rc;
-    return launch_any<kFmtInt8, false>(p, q, w, K, M, sms, static_cast<cudaStream_t>(stream));
+    return launch_any<kFmtInt8, false>(p, q, w, M, sms, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int skinny_tile_device_error(int clear, unsigned* flags)

@@ -72,6 +72,11 @@ CASES = [
     ("fp8", 131, 272, [0, 7, 0, 31, 2]),
     ("fp8", 128, 1408, [90, 0, 130]),
     ("fp8", 77, 400, [600, 3]),
+    ("nvfp4", 129, 1040, [10, 20, 13]),
+    ("fp8", 129, 272, [30, 40, 1]),
+    ("nvfp4", 260, 1040, [60, 50, 70]),
+    ("fp8", 260, 400, [60, 50, 70]),
+    ("nvfp4", 2000, 400, [400, 390, 5, 7, 300]),         # whole tiles next to split ones
 ]
 
 
