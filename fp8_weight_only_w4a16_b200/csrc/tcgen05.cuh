@@ -48,11 +48,11 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar)
 }
 
 // Shared-memory operand descriptor: K-major rows of 128 bytes in the 128-byte
-// swizzle that a tiled TMA load writes (8-row groups 1024 bytes apart).
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr)
-{
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
+// swizzle that a tiled TMA load writes (8-row groups 1024 bytes apart).  The
+// high word is constant; the low word holds the address in units of 16 bytes,
+// so 32 bytes further along K is + 2.
+constexpr uint32_t kSmemDescHigh = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t smem_desc_low(uint32_t addr) { return (addr >> 4) | (1u << 16); }
 
 // Instruction descriptor of a 128 x n matrix instruction, both operands K-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int n)   // f16 x f16 -> f32
@@ -64,25 +64,29 @@ __host__ __device__ constexpr uint32_t idesc_s8(int n)    // s8 x s8 -> s32
     return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-// D[tmem] (+)= A[tmem, 128 x 16 f16] . B[smem, n x 16 f16]^T
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+// D[tmem] (+)= A[tmem, 128 x 16 f16] . B[smem, n x 16 f16]^T; b is the low
+// word of B's descriptor.  `add` is a constant wherever it can be.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 bd;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "mov.b64 bd, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(add), "n"(kSmemDescHigh)
         : "memory");
 }
 
 // D[tmem] (+)= A[smem, 128 x 32 s8] . B[smem, n x 32 s8]^T
-__device__ __forceinline__ void mma_s8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void mma_s8_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "mov.b64 ad, {%1, %5};\n\t"
+        "mov.b64 bd, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], ad, bd, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(add), "n"(kSmemDescHigh)
         : "memory");
 }
 

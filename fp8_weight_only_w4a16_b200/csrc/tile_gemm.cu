@@ -96,11 +96,14 @@ struct Cfg {
     static constexpr int kWBytes = block_bytes(FMT) * kWBlocks;
     static constexpr int kChunkBytes = TN * 128;
     static constexpr int kXBytes = kChunkBytes * kXChunks;
-    // Tensor memory: two accumulators at columns 0 and TN, then the decoded
-    // blocks, 64 columns each, at the end.
+    // Tensor memory: two accumulators at columns 0 and TN, then two stages of
+    // decoded blocks, 64 columns a block, at the end.  A stage has two blocks
+    // where they fit: the MMA thread's waits and commits cost it ~300 clocks a
+    // stage, next to ~400 in which a block arrives from HBM.
     static constexpr int kDStages = 2;
-    static constexpr int kAStages = kInt8 ? 0 : TN > 128 ? 2 : 4;
-    static constexpr int kACol = 512 - 64 * kAStages;
+    static constexpr int kABlocks = kInt8 ? kWBlocks : TN > 128 ? 1 : 2;        // blocks per step of the MMA thread
+    static constexpr int kAStages = kInt8 ? 0 : 2;
+    static constexpr int kACol = 512 - 64 * kABlocks * kAStages;
     // Groups of four decoder warps, which take turns: while one group waits
     // for its stores, the others convert.
     static constexpr int kGroups = kInt8 ? 0 : 2;
@@ -121,7 +124,8 @@ struct Cfg {
     static constexpr int kBytes = kBarOff + kBars * 8 + 1024;   // + alignment of the dynamic shared memory
     static_assert(kBytes + 8 * (kMaxExperts + 2) + 256 <= 232448, "shared memory per CTA");
     static_assert(kDStages * TN <= kACol, "accumulators and decoded blocks overlap");
-    static_assert(kAStages >= kGroups, "a decoder group fills one stage at a time");
+    static_assert(kInt8 || kAStages == kGroups, "a decoder group fills the same stage every time");
+    static_assert(kWBlocks % kABlocks == 0 && kABlocks * kChunksPerBlock % kXChunks == 0, "slots nest");
     static_assert(kXBytes % 1024 == 0 && kWBytes % 1024 == 0, "swizzled tiles start on 1024 bytes");
     static_assert(kXStages >= 2 && kWStages >= 2, "rings");
 };
@@ -337,10 +341,21 @@ __device__ void make_schedule(Schedule& s, const Params& p)
     if (i == p.E - 1) s.total = (int)n;
 }
 
-__device__ __forceinline__ void store_out(void* y, int64_t at, float v, int f32)
+// Stores r[0..n) at y[at], y[at + step], ...
+template <int N>
+__device__ __forceinline__ void put_column(void* y, int64_t at, int step, const float (&r)[N], int n, int f32)
 {
-    if (f32) static_cast<float*>(y)[at] = v;
-    else static_cast<__half*>(y)[at] = __float2half_rn(v);
+    if (f32) {
+        float* p = static_cast<float*>(y) + at;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j < n) p[(int64_t)j * step] = r[j];
+    } else {
+        __half* p = static_cast<__half*>(y) + at;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j < n) p[(int64_t)j * step] = __float2half_rn(r[j]);
+    }
 }
 
 template <int FMT, int TN, bool SILU>
@@ -362,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         }
         for (int i = 0; i < C::kWStages; ++i) {
             ptx::mbar_init(sm.w_full(i), 1);
-            ptx::mbar_init(sm.w_empty(i), C::kInt8 ? 1 : 4 * C::kWBlocks);
+            ptx::mbar_init(sm.w_empty(i), C::kInt8 ? 1 : 4 * C::kWBlocks / C::kABlocks);
         }
         for (int i = 0; i < C::kAStages; ++i) {
             ptx::mbar_init(sm.a_full(i), 4);
@@ -493,59 +508,54 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         // ---- MMA: one thread issues
         if (ptx::elect_one()) {
             mine = true;
-            Ring xr, wr, ar, dr;
+            Ring xr, ar, dr;      // ar: decoded stages (int8: weight slots)
+            constexpr int kAN = C::kInt8 ? C::kWStages : C::kAStages;
+            constexpr int kChunks = C::kABlocks * C::kChunksPerBlock;
+            const uint32_t x0 = ptx::smem_desc_low(ptx::smem_addr(sm.x(0)));
+            const uint32_t a0 = C::kInt8 ? ptx::smem_desc_low(ptx::smem_addr(sm.w(0))) : tmem + C::kACol;
+            constexpr uint32_t kXStep = C::kXBytes >> 4, kAStep = C::kInt8 ? C::kWBytes >> 4 : 64 * C::kABlocks;
+            constexpr uint32_t kXChunkStep = C::kChunkBytes >> 4, kAChunkStep = C::kInt8 ? block_bytes(FMT) >> 4 : 32;
+            uint32_t xd = x0, ad = a0;
             bool ok = true;
             while (ok && walk.next(g)) {
                 ok = wait(sm.d_empty(dr.i), dr.phase ^ 1, &s.abort, kErrAccumulator);
                 if (!ok) break;
-                ptx::tc_fence_after();
                 const int n16 = (g.n + 15) & ~15;
                 const uint32_t d = tmem + dr.i * TN;
                 const uint32_t idesc = C::kInt8 ? ptx::idesc_s8(n16) : ptx::idesc_f16(n16);
-                int xc = 0;      // piece within the token slot
-                for (int k = g.k0; ok && k < g.k1; ++k) {
-                    const int wb = (k - g.k0) % C::kWBlocks;
-                    const bool last = k + 1 == g.k1;
-                    if constexpr (C::kInt8) {
-                        if (wb == 0) ok = wait(sm.w_full(wr.i), wr.phase, &s.abort, kErrRing);
-                    } else {
-                        ok = wait(sm.a_full(ar.i), ar.phase, &s.abort, kErrRing);
-                    }
-                    if (!ok) break;
+                uint32_t add = 0;
+                for (int k = g.k0; ok && k < g.k1; k += C::kABlocks) {
+                    ok = wait(C::kInt8 ? sm.w_full(ar.i) : sm.a_full(ar.i), ar.phase, &s.abort, kErrRing);
+                    const int chunks = (k + C::kABlocks <= g.k1 ? C::kABlocks : g.k1 - k) * C::kChunksPerBlock;
 #pragma unroll
-                    for (int h = 0; h < C::kChunksPerBlock; ++h) {
-                        if (xc == 0) ok = wait(sm.x_full(xr.i), xr.phase, &s.abort, kErrRing);
-                        if (!ok) break;
-                        ptx::tc_fence_after();
-                        const uint64_t b = ptx::smem_desc_sw128(ptx::smem_addr(sm.x(xr.i) + xc * C::kChunkBytes));
-                        if constexpr (C::kInt8) {
-                            const uint64_t a =
-                                ptx::smem_desc_sw128(ptx::smem_addr(sm.w(wr.i) + wb * block_bytes(FMT)));
+                    for (int c = 0; c < kChunks; ++c) {
+                        if (c < chunks && ok) {
+                            if (c % C::kXChunks == 0) {
+                                ok = wait(sm.x_full(xr.i), xr.phase, &s.abort, kErrRing);
+                                ptx::tc_fence_after();
+                            }
+                            if (ok) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                ptx::mma_s8_ss(d, a + 2 * j, b + 2 * j, idesc, k > g.k0 || j > 0);
-                        } else {
-                            const uint32_t a = tmem + C::kACol + ar.i * 64;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                ptx::mma_f16_ts(d, a + 32 * h + 8 * j, b + 2 * j, idesc, k > g.k0 || h > 0 || j > 0);
-                        }
-                        if (++xc == C::kXChunks || (last && h == C::kChunksPerBlock - 1)) {
-                            ptx::tc_commit(sm.x_empty(xr.i));
-                            xr.step(C::kXStages);
-                            xc = 0;
+                                for (int j = 0; j < 4; ++j) {
+                                    const uint32_t b = xd + c % C::kXChunks * kXChunkStep + 2 * j;
+                                    const uint32_t more = c == 0 && j == 0 ? add : 1u;
+                                    if constexpr (C::kInt8)
+                                        ptx::mma_s8_ss(d, ad + c * kAChunkStep + 2 * j, b, idesc, more);
+                                    else
+                                        ptx::mma_f16_ts(d, ad + c * kAChunkStep + 8 * j, b, idesc, more);
+                                }
+                            }
+                            if ((c + 1) % C::kXChunks == 0 || c + 1 == chunks) {
+                                ptx::tc_commit(sm.x_empty(xr.i));
+                                xr.step(C::kXStages);
+                                xd = xr.i == 0 ? x0 : xd + kXStep;
+                            }
                         }
                     }
-                    if (!ok) break;
-                    if constexpr (C::kInt8) {
-                        if (wb == C::kWBlocks - 1 || last) {
-                            ptx::tc_commit(sm.w_empty(wr.i));
-                            wr.step(C::kWStages);
-                        }
-                    } else {
-                        ptx::tc_commit(sm.a_empty(ar.i));
-                        ar.step(C::kAStages);
-                    }
+                    add = 1;
+                    ptx::tc_commit(C::kInt8 ? sm.w_empty(ar.i) : sm.a_empty(ar.i));
+                    ar.step(kAN);
+                    ad = ar.i == 0 ? a0 : ad + kAStep;
                 }
                 if (!ok) break;
                 ptx::tc_commit(sm.d_full(dr.i));
@@ -555,13 +565,15 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
     } else if (warp >= 4 && warp < 4 + C::kDecodeWarps) {
         // ---- decoders: thread = weight row (warp % 4, lane); the groups take blocks in turn
         if constexpr (!C::kInt8) {
-            Ring wr, ar;
+            Ring wr;
             const int row = (warp & 3) * 32 + lane;
-            int turn = (warp - 4) >> 2;      // blocks until this group's next
-            const uint32_t dst = tmem + ((uint32_t)(warp & 3) << 21) + C::kACol;
+            const int group = (warp - 4) >> 2;      // fills decoded stage `group`, every kGroups-th step
+            const uint32_t dst = tmem + ((uint32_t)(warp & 3) << 21) + C::kACol + group * 64 * C::kABlocks;
+            int turn = group;                       // steps until this group's next
+            uint32_t a_phase = 1;
             bool ok = true;
             while (ok && walk.next(g)) {
-                for (int k = g.k0; k < g.k1; ++k) {
+                for (int k = g.k0; k < g.k1; k += C::kABlocks) {
                     const int wb = (k - g.k0) % C::kWBlocks;
                     const bool alone = wb == 0 && k + 1 == g.k1;      // a slot with one block
                     if (turn == 0) {
@@ -571,60 +583,71 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                             ok = false;
                             break;
                         }
-                        const uint32_t src = ptx::smem_addr(sm.w(wr.i) + wb * block_bytes(FMT));
-                        constexpr int kWords = FMT == SKINNY_FMT_NVFP4 ? 4 : 8;
-                        uint4 c[kWords];
 #pragma unroll
-                        for (int i = 0; i < kWords; ++i) c[i] = ptx::lds128(src + (i * kRows + row) * 16);
-                        uint32_t sc[2] = {0, 0};
-                        if constexpr (FMT == SKINNY_FMT_NVFP4) ptx::lds64(src + kNvfp4BlockScales + row * 8, sc);
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive_n(sm.w_empty(wr.i), alone ? C::kWBlocks : 1);
-                        ok = wait(sm.a_empty(ar.i), ar.phase ^ 1, &s.abort, kErrRing);
-                        if (!__all_sync(~0u, ok)) {
-                            ok = false;
-                            break;
-                        }
-                        ptx::tc_fence_after();
+                        for (int b = 0; b < C::kABlocks; ++b) {
+                            if (b > 0 && alone) break;
+                            const uint32_t src = ptx::smem_addr(sm.w(wr.i) + (wb + b) * block_bytes(FMT));
+                            constexpr int kWords = FMT == SKINNY_FMT_NVFP4 ? 4 : 8;
+                            uint4 c[kWords];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t v[32];
-                            if constexpr (FMT == SKINNY_FMT_NVFP4) {
-                                uint32_t s01, s23;
-                                ptx::e4m3x4_to_f16x4(sc[h], s01, s23);
-                                const uint32_t sd[4] = {ptx::dup_lo(s01), ptx::dup_hi(s01), ptx::dup_lo(s23),
-                                                        ptx::dup_hi(s23)};
-                                const uint32_t words[8] = {c[2 * h].x,     c[2 * h].y,     c[2 * h].z,
-                                                           c[2 * h].w,     c[2 * h + 1].x, c[2 * h + 1].y,
-                                                           c[2 * h + 1].z, c[2 * h + 1].w};
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    uint32_t f[4];
-                                    ptx::e2m1x8_to_f16x8(words[i], f);
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) v[4 * i + j] = ptx::hmul2(f[j], sd[i / 2]);
-                                }
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const uint4 w = c[4 * h + i];
-                                    ptx::e4m3x4_to_f16x4(w.x, v[8 * i], v[8 * i + 1]);
-                                    ptx::e4m3x4_to_f16x4(w.y, v[8 * i + 2], v[8 * i + 3]);
-                                    ptx::e4m3x4_to_f16x4(w.z, v[8 * i + 4], v[8 * i + 5]);
-                                    ptx::e4m3x4_to_f16x4(w.w, v[8 * i + 6], v[8 * i + 7]);
-                                }
+                            for (int i = 0; i < kWords; ++i) c[i] = ptx::lds128(src + (i * kRows + row) * 16);
+                            uint32_t sc[2] = {0, 0};
+                            if constexpr (FMT == SKINNY_FMT_NVFP4)
+                                ptx::lds64(src + kNvfp4BlockScales + row * 8, sc);
+                            if (b + 1 == C::kABlocks || alone) {
+                                __syncwarp();
+                                if (lane == 0)
+                                    ptx::mbar_arrive_n(sm.w_empty(wr.i), alone ? C::kWBlocks / C::kABlocks : 1);
                             }
-                            ptx::tmem_st32(dst + ar.i * 64 + h * 32, v);
+                            if (b == 0) {
+                                ok = wait(sm.a_empty(group), a_phase, &s.abort, kErrRing);
+                                a_phase ^= 1;
+                                if (!__all_sync(~0u, ok)) {
+                                    ok = false;
+                                    break;
+                                }
+                                ptx::tc_fence_after();
+                            }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t v[32];
+                                if constexpr (FMT == SKINNY_FMT_NVFP4) {
+                                    uint32_t s01, s23;
+                                    ptx::e4m3x4_to_f16x4(sc[h], s01, s23);
+                                    const uint32_t sd[4] = {ptx::dup_lo(s01), ptx::dup_hi(s01), ptx::dup_lo(s23),
+                                                            ptx::dup_hi(s23)};
+                                    const uint32_t words[8] = {c[2 * h].x,     c[2 * h].y,     c[2 * h].z,
+                                                               c[2 * h].w,     c[2 * h + 1].x, c[2 * h + 1].y,
+                                                               c[2 * h + 1].z, c[2 * h + 1].w};
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) {
+                                        uint32_t f[4];
+                                        ptx::e2m1x8_to_f16x8(words[i], f);
+#pragma unroll
+                                        for (int j = 0; j < 4; ++j) v[4 * i + j] = ptx::hmul2(f[j], sd[i / 2]);
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const uint4 w = c[4 * h + i];
+                                        ptx::e4m3x4_to_f16x4(w.x, v[8 * i], v[8 * i + 1]);
+                                        ptx::e4m3x4_to_f16x4(w.y, v[8 * i + 2], v[8 * i + 3]);
+                                        ptx::e4m3x4_to_f16x4(w.z, v[8 * i + 4], v[8 * i + 5]);
+                                        ptx::e4m3x4_to_f16x4(w.w, v[8 * i + 6], v[8 * i + 7]);
+                                    }
+                                }
+                                ptx::tmem_st32(dst + b * 64 + h * 32, v);
+                            }
                         }
+                        if (!ok) break;
                         ptx::tmem_wait_st();
                         ptx::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(sm.a_full(ar.i));
+                        if (lane == 0) ptx::mbar_arrive(sm.a_full(group));
                     } else {
                         --turn;
                     }
-                    ar.step(C::kAStages);
-                    if (wb == C::kWBlocks - 1 || k + 1 == g.k1) wr.step(C::kWStages);
+                    if (wb + C::kABlocks == C::kWBlocks || k + C::kABlocks >= g.k1) wr.step(C::kWStages);
                 }
             }
         }
@@ -678,6 +701,10 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                 else scale = p.scale[o];
             }
             for (int c0 = 0; c0 < g.n; c0 += 32) {
+                // Everything loaded here is loaded before the first store: the
+                // compiler cannot move a load across one.
+                float rs = 0.f;
+                if (C::kInt8 && !publish && c0 + lane < g.n) rs = p.row_scale[g.t0 + c0 + lane];
                 uint32_t v[32];
                 if constexpr (TN == 16) {
                     uint32_t lo[16];
@@ -687,46 +714,47 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                 } else {
                     ptx::tmem_ld32(src + dr.i * TN + c0, v);
                 }
+                const int left = g.n - c0;
                 if (publish) {
-                    unsigned* slot = p.partials + (size_t)blockIdx.x * kSlotWords + row;
+                    unsigned* slot = p.partials + (size_t)blockIdx.x * kSlotWords + row + c0 * kRows;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (c0 + j < g.n) slot[(c0 + j) * kRows] = v[j];
+                        if (j < left) slot[j * kRows] = v[j];
                     continue;
                 }
                 for (int c = blockIdx.x - 1; c >= lowest; --c) {
                     if (walk.empty(c)) continue;
-                    const unsigned* slot = p.partials + (size_t)c * kSlotWords + row;
+                    const unsigned* slot = p.partials + (size_t)c * kSlotWords + row + c0 * kRows;
                     uint32_t o32[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o32[j] = c0 + j < g.n ? __ldcg(slot + (c0 + j) * kRows) : 0;
+                    for (int j = 0; j < 32; ++j) o32[j] = j < left ? __ldcg(slot + j * kRows) : 0;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         v[j] = C::kInt8 ? v[j] + o32[j]
                                         : __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(o32[j]));
                 }
+                // y of this thread's channel at the chunk's first token
+                const int64_t at = (int64_t)(g.t0 + c0) * p.outputs + o;
                 if constexpr (SILU) {
+                    float r[16];
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         // lanes 0..15 finish token j, lanes 16..31 token j + 1
                         const float a = __uint_as_float(v[j]) * scale, b = __uint_as_float(v[j + 1]) * scale;
                         const float other = __shfl_xor_sync(~0u, lane < 16 ? b : a, 16);
                         const float gate = lane < 16 ? a : other, up = lane < 16 ? other : b;
-                        const int t = c0 + j + (lane >> 4);
-                        if (valid && t < g.n)
-                            store_out(p.y, (int64_t)(g.t0 + t) * p.outputs + o, gate / (1.f + expf(-gate)) * up,
-                                      p.out_f32);
+                        r[j / 2] = gate / (1.f + expf(-gate)) * up;
                     }
+                    put_column<16>(p.y, at + (lane >> 4) * p.outputs, 2 * p.outputs, r,
+                                   valid ? (left + 1 - (lane >> 4)) / 2 : 0, p.out_f32);
                 } else {
+                    float r[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        const int t = c0 + j;
-                        if (valid && t < g.n) {
-                            const float r = C::kInt8 ? (float)(int)v[j] * p.row_scale[g.t0 + t] * scale
-                                                     : __uint_as_float(v[j]) * scale;
-                            store_out(p.y, (int64_t)(g.t0 + t) * p.outputs + o, r, p.out_f32);
-                        }
+                        if constexpr (C::kInt8) r[j] = (float)(int)v[j] * __shfl_sync(~0u, rs, j) * scale;
+                        else r[j] = __uint_as_float(v[j]) * scale;
                     }
+                    put_column<32>(p.y, at, p.outputs, r, valid ? left : 0, p.out_f32);
                 }
             }
             ptx::tc_fence_before();
