@@ -120,14 +120,11 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n)
+__device__ __forceinline__ uint32_t lds32(uint32_t addr)
 {
-    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
-}
-
-__device__ __forceinline__ void lds64(uint32_t addr, uint32_t (&v)[2])
-{
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr) : "memory");
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map)

@@ -81,53 +81,52 @@ struct Params {
 
 constexpr int at_most(int a, int b) { return a < b ? a : b; }
 
+// A step is what one turn of every role handles: two K blocks of a narrow
+// tile, one of a wide one.  Per step the MMA thread waits for one barrier,
+// issues and commits to one barrier: each further wait or commit costs it
+// some hundred clocks (its code competes with the decoders' for the
+// instruction caches), and a narrow step has to fit in the ~800 clocks in
+// which its weights arrive from HBM.
 template <int FMT, int TN>
 struct Cfg {
     static constexpr bool kInt8 = FMT == kFmtInt8;
-    // A TMA or bulk copy costs its issuing thread 100 to 200 ns whatever its
-    // size, and narrow tiles leave a block only ~200 ns, so their ring slots
-    // hold two blocks of weights (one copy) and of tokens (one copy).
-    static constexpr int kWBlocks = (kInt8 && TN > 64) ? 1 : 2;                 // blocks per weight slot
+    static constexpr int kStepBlocks = TN > 64 ? 1 : 2;
     static constexpr int kChunksPerBlock = kInt8 ? 1 : 2;                       // 128-byte wide pieces of x per block
-    static constexpr int kXChunks = TN > 64 ? 1 : 2 * kChunksPerBlock;          // pieces per token slot
-    static constexpr bool kX3d = kXChunks > 1;
-    static constexpr int kSmallBox = TN / 4;                                    // tokens of the small box (TN > 64)
-    static constexpr int kXProducers = TN > 64 ? 2 : 1;
-    static constexpr int kWBytes = block_bytes(FMT) * kWBlocks;
+    static constexpr int kChunks = kStepBlocks * kChunksPerBlock;               // pieces per step
+    static constexpr int kWBytes = block_bytes(FMT) * kStepBlocks;              // a weight slot
     static constexpr int kChunkBytes = TN * 128;
-    static constexpr int kXBytes = kChunkBytes * kXChunks;
-    // Tensor memory: two accumulators at columns 0 and TN, then two stages of
-    // decoded blocks, 64 columns a block, at the end.  A stage has two blocks
-    // where they fit: the MMA thread's waits and commits cost it ~300 clocks a
-    // stage, next to ~400 in which a block arrives from HBM.
+    static constexpr int kXBytes = kChunkBytes * kChunks;                       // a token slot
+    // A narrow tile's tokens arrive in one box per step, a wide one's in boxes
+    // of a quarter of its columns, as many as it has tokens.
+    static constexpr bool kX3d = TN <= 64;
+    static constexpr bool kW3d = kInt8 && kStepBlocks == 2;
+    static constexpr int kBox = kX3d ? TN : TN / 4;
+    // Tensor memory: two accumulators at columns 0 and TN, then a stage of
+    // decoded blocks, 64 columns a block, for each group of decoder warps.
     static constexpr int kDStages = 2;
-    static constexpr int kABlocks = kInt8 ? kWBlocks : TN > 128 ? 1 : 2;        // blocks per step of the MMA thread
-    static constexpr int kAStages = kInt8 ? 0 : 2;
-    static constexpr int kACol = 512 - 64 * kABlocks * kAStages;
-    // Groups of four decoder warps, which take turns: while one group waits
-    // for its stores, the others convert.
     static constexpr int kGroups = kInt8 ? 0 : 2;
+    static constexpr int kACol = 512 - 64 * kStepBlocks * kGroups;
     static constexpr int kDecodeWarps = 4 * kGroups;
     static constexpr int kWarps = 4 + kDecodeWarps + 4;
     static constexpr int kThreads = kWarps * 32;
-    // Ring slots: tokens for about as many blocks as weights; next to wide
-    // token slots the weights' ring stays short.
+    // Ring slots.  Experts: weights first, up to what hides HBM's latency (150
+    // KB; a wide tile asks for less), and the tokens' ring takes the rest.
+    // int8 slots hold weights and tokens.
     static constexpr int kBudget = 218 * 1024;
-    static constexpr int kXPerW = kWBlocks * kChunksPerBlock / kXChunks;        // token slots per weight slot
-    static constexpr int kWStages = !kInt8 && TN > 64 ? (FMT == SKINNY_FMT_NVFP4 ? 4 : 3)
-                                                      : at_most(kBudget / (kWBytes + kXPerW * kXBytes), 10);
-    static constexpr int kXStages = at_most((kBudget - kWStages * kWBytes) / kXBytes, 16);
+    static constexpr int kWTarget = (TN > 64 ? 72 : 150) * 1024;
+    static constexpr int kWStages = kInt8 ? at_most(kBudget / (kWBytes + kXBytes), 12)
+                                          : at_most((kBudget - 3 * kXBytes) / kWBytes, kWTarget / kWBytes);
+    static constexpr int kXStages = kInt8 ? kWStages : at_most((kBudget - kWStages * kWBytes) / kXBytes, 12);
     static constexpr int kXOff = 0;
     static constexpr int kWOff = kXStages * kXBytes;
     static constexpr int kBarOff = kWOff + kWStages * kWBytes;
-    static constexpr int kBars = 2 * (kXStages + kWStages + kAStages + kDStages) + 1;
+    static constexpr int kBars = 2 * (kXStages + kWStages + kDStages) + kGroups + 1;
     static constexpr int kBytes = kBarOff + kBars * 8 + 1024;   // + alignment of the dynamic shared memory
     static_assert(kBytes + 8 * (kMaxExperts + 2) + 256 <= 232448, "shared memory per CTA");
     static_assert(kDStages * TN <= kACol, "accumulators and decoded blocks overlap");
-    static_assert(kInt8 || kAStages == kGroups, "a decoder group fills the same stage every time");
-    static_assert(kWBlocks % kABlocks == 0 && kABlocks * kChunksPerBlock % kXChunks == 0, "slots nest");
-    static_assert(kXBytes % 1024 == 0 && kWBytes % 1024 == 0, "swizzled tiles start on 1024 bytes");
-    static_assert(kXStages >= 2 && kWStages >= 2, "rings");
+    static_assert(kChunkBytes % 1024 == 0 && kWBytes % 1024 == 0 && kBox * 128 % 1024 == 0,
+                  "swizzled tiles start on 1024 bytes");
+    static_assert(kXStages >= 3 && kWStages >= 3, "rings");
 };
 
 // The tile sequence, from the experts' row counts: expert e has
@@ -260,12 +259,11 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* abort,
     return wait_slow(bar, parity, abort, code);
 }
 
-// Waits for a producer's copies in flight: of the slots before position r,
-// at most one round, every one that it filled (it fills one in `stride`).
-__device__ __noinline__ void drain(Ring r, int issued, int stride, int stages, uint64_t* full)
+// Waits for a producer's copies in flight: the last `issued` slots before
+// position r, at most one round.
+__device__ __noinline__ void drain(Ring r, int issued, int stages, uint64_t* full)
 {
-    const int n = issued * stride < stages ? issued * stride : stages;
-    for (int k = n; k > 0; --k) {
+    for (int k = issued < stages ? issued : stages; k > 0; --k) {
         if (r.i == 0) {
             r.i = stages;
             r.phase ^= 1;
@@ -282,14 +280,15 @@ struct Shared {
     __device__ uint8_t* x(int i) const { return base + C::kXOff + i * C::kXBytes; }
     __device__ uint8_t* w(int i) const { return base + C::kWOff + i * C::kWBytes; }
     __device__ uint64_t* bars() const { return reinterpret_cast<uint64_t*>(base + C::kBarOff); }
+    // full: the copies have landed.  x_empty: the step's matrix instructions are
+    // done (which also frees the decoded stage that they read, and int8's weights).
     __device__ uint64_t* x_full(int i) const { return bars() + i; }
     __device__ uint64_t* x_empty(int i) const { return bars() + C::kXStages + i; }
     __device__ uint64_t* w_full(int i) const { return bars() + 2 * C::kXStages + i; }
     __device__ uint64_t* w_empty(int i) const { return bars() + 2 * C::kXStages + C::kWStages + i; }
-    __device__ uint64_t* a_full(int i) const { return bars() + 2 * (C::kXStages + C::kWStages) + i; }
-    __device__ uint64_t* a_empty(int i) const { return a_full(i) + C::kAStages; }
-    __device__ uint64_t* d_full(int i) const { return bars() + 2 * (C::kXStages + C::kWStages + C::kAStages) + i; }
+    __device__ uint64_t* d_full(int i) const { return bars() + 2 * (C::kXStages + C::kWStages) + i; }
     __device__ uint64_t* d_empty(int i) const { return d_full(i) + C::kDStages; }
+    __device__ uint64_t* a_full(int i) const { return bars() + 2 * (C::kXStages + C::kWStages + C::kDStages) + i; }
     __device__ uint64_t* drained() const { return bars() + C::kBars - 1; }
 };
 
@@ -372,17 +371,14 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kXStages; ++i) {
-            ptx::mbar_init(sm.x_full(i), 1);
+            ptx::mbar_init(sm.x_full(i), C::kInt8 ? 2 : 1);      // int8: both producers' copies
             ptx::mbar_init(sm.x_empty(i), 1);
         }
         for (int i = 0; i < C::kWStages; ++i) {
             ptx::mbar_init(sm.w_full(i), 1);
-            ptx::mbar_init(sm.w_empty(i), C::kInt8 ? 1 : 4 * C::kWBlocks / C::kABlocks);
+            ptx::mbar_init(sm.w_empty(i), 4);
         }
-        for (int i = 0; i < C::kAStages; ++i) {
-            ptx::mbar_init(sm.a_full(i), 4);
-            ptx::mbar_init(sm.a_empty(i), 1);
-        }
+        for (int i = 0; i < C::kGroups; ++i) ptx::mbar_init(sm.a_full(i), 4);
         for (int i = 0; i < C::kDStages; ++i) {
             ptx::mbar_init(sm.d_full(i), 1);
             ptx::mbar_init(sm.d_empty(i), 4);
@@ -415,7 +411,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
     const uint32_t tmem = s.tmem;
     Walk<TN> walk(s, p);
     Segment g;
-    Ring r;            // the producers' position and how much they have issued
+    Ring r;            // position of a single-thread role, and how much it has issued
     int issued = 0;
     // The single-thread roles run under elect.sync, which tells the compiler
     // that one thread is active: a matrix instruction of 16 columns then issues
@@ -431,23 +427,22 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             while (ok && walk.next(g)) {
                 const uint8_t* src =
                     C::kInt8 ? nullptr : p.w + ((size_t)g.e * p.G + g.row_tile) * p.C * block_bytes(FMT);
-                for (int k = g.k0; k < g.k1; k += C::kWBlocks) {
-                    if (!wait(sm.w_empty(r.i), r.phase ^ 1, &s.abort, kErrRing)) {
-                        ok = false;
-                        break;
-                    }
+                for (int k = g.k0; k < g.k1; k += C::kStepBlocks) {
+                    ok = wait(C::kInt8 ? sm.x_empty(r.i) : sm.w_empty(r.i), r.phase ^ 1, &s.abort, kErrRing);
+                    if (!ok) break;
                     if constexpr (C::kInt8) {
-                        ptx::mbar_arrive_expect_tx(sm.w_full(r.i), C::kWBytes);
-                        if (C::kWBlocks == 2 && (k + 2) * kBlockK <= p.K) {
-                            ptx::tma_load_3d(sm.w(r.i), &w_map, 0, g.row_tile * kRows, k, sm.w_full(r.i), pol);
+                        uint64_t* full = sm.x_full(r.i);
+                        ptx::mbar_arrive_expect_tx(full, C::kWBytes);
+                        if (C::kW3d && (k + 2) * kBlockK <= p.K) {
+                            ptx::tma_load_3d(sm.w(r.i), &w_map, 0, g.row_tile * kRows, k, full, pol);
                         } else {
                             // plain boxes: past K they fill in zeros
-                            for (int b = 0; b < C::kWBlocks; ++b)
-                                ptx::tma_load_2d(sm.w(r.i) + b * block_bytes(FMT), C::kWBlocks == 2 ? &w_map2 : &w_map,
-                                                 (k + b) * kBlockK, g.row_tile * kRows, sm.w_full(r.i), pol);
+                            for (int b = 0; b < C::kStepBlocks; ++b)
+                                ptx::tma_load_2d(sm.w(r.i) + b * block_bytes(FMT), C::kW3d ? &w_map2 : &w_map,
+                                                 (k + b) * kBlockK, g.row_tile * kRows, full, pol);
                         }
                     } else {
-                        const uint32_t bytes = (k + 1 < g.k1 ? 2 : 1) * block_bytes(FMT);
+                        const uint32_t bytes = (C::kStepBlocks == 2 && k + 1 < g.k1 ? 2 : 1) * block_bytes(FMT);
                         ptx::mbar_arrive_expect_tx(sm.w_full(r.i), bytes);
                         ptx::bulk_g2s(sm.w(r.i), src + (size_t)k * block_bytes(FMT), bytes, sm.w_full(r.i), pol);
                     }
@@ -456,48 +451,39 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                 }
             }
         }
-    } else if (warp == 1 || (warp == 3 && C::kXProducers == 2)) {
-        // ---- x producers: two take turns where the slots are small for their time
+    } else if (warp == 1) {
+        // ---- x producer
         if (ptx::elect_one()) {
             mine = true;
             bool ok = true;
             const uint64_t pol = TN <= 32 ? ptx::policy_evict_last() : ptx::policy_evict_normal();
             if (C::kInt8) ptx::pdl_wait_prior_grid();
-            int turn = warp == 1 ? 0 : 1;
             constexpr int kChunkK = kBlockK / C::kChunksPerBlock;
             const int whole = p.K / kChunkK;      // pieces that lie within K entirely
             while (ok && walk.next(g)) {
                 const int c1 = g.k1 * C::kChunksPerBlock;
-                for (int c = g.k0 * C::kChunksPerBlock; c < c1; c += C::kXChunks) {
-                    if (C::kXProducers == 2 && (turn ^= 1) == 0) {
-                        r.step(C::kXStages);
-                        continue;
-                    }
-                    if (!wait(sm.x_empty(r.i), r.phase ^ 1, &s.abort, kErrRing)) {
-                        ok = false;
-                        break;
-                    }
+                const int boxes = (g.n + C::kBox - 1) / C::kBox;
+                for (int c = g.k0 * C::kChunksPerBlock; c < c1; c += C::kChunks) {
+                    ok = wait(sm.x_empty(r.i), r.phase ^ 1, &s.abort, kErrRing);
+                    if (!ok) break;
                     if constexpr (C::kX3d) {
-                        // one box of kXChunks pieces; where K ends inside one, a box for each
+                        // one box of kChunks pieces; where K ends inside one, a box for each
                         // piece, which fills in zeros past K
                         ptx::mbar_arrive_expect_tx(sm.x_full(r.i), C::kXBytes);
-                        const int last = c + C::kXChunks < c1 ? c + C::kXChunks : c1;
+                        const int last = c + C::kChunks < c1 ? c + C::kChunks : c1;
                         if (last <= whole) {
                             ptx::tma_load_3d(sm.x(r.i), &x_map, 0, g.t0, c, sm.x_full(r.i), pol);
                         } else {
-                            for (int b = 0; b < C::kXChunks; ++b)
+                            for (int b = 0; b < C::kChunks; ++b)
                                 ptx::tma_load_2d(sm.x(r.i) + b * C::kChunkBytes, &x_map2, (c + b) * kChunkK, g.t0,
                                                  sm.x_full(r.i), pol);
                         }
-                    } else if (g.n > 2 * C::kSmallBox) {
-                        ptx::mbar_arrive_expect_tx(sm.x_full(r.i), C::kXBytes);
-                        ptx::tma_load_2d(sm.x(r.i), &x_map, c * kChunkK, g.t0, sm.x_full(r.i), pol);
                     } else {
-                        const int boxes = g.n > C::kSmallBox ? 2 : 1;
-                        ptx::mbar_arrive_expect_tx(sm.x_full(r.i), boxes * C::kSmallBox * 128);
-                        for (int b = 0; b < boxes; ++b)
-                            ptx::tma_load_2d(sm.x(r.i) + b * C::kSmallBox * 128, &x_map2, c * kChunkK,
-                                             g.t0 + b * C::kSmallBox, sm.x_full(r.i), pol);
+                        ptx::mbar_arrive_expect_tx(sm.x_full(r.i), C::kChunks * boxes * C::kBox * 128);
+                        for (int h = 0; h < C::kChunks; ++h)
+                            for (int b = 0; b < boxes; ++b)
+                                ptx::tma_load_2d(sm.x(r.i) + h * C::kChunkBytes + b * C::kBox * 128, &x_map,
+                                                 (c + h) * kChunkK, g.t0 + b * C::kBox, sm.x_full(r.i), pol);
                     }
                     r.step(C::kXStages);
                     ++issued;
@@ -508,14 +494,15 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         // ---- MMA: one thread issues
         if (ptx::elect_one()) {
             mine = true;
-            Ring xr, ar, dr;      // ar: decoded stages (int8: weight slots)
-            constexpr int kAN = C::kInt8 ? C::kWStages : C::kAStages;
-            constexpr int kChunks = C::kABlocks * C::kChunksPerBlock;
+            Ring dr;
+            constexpr uint32_t kXStep = C::kXBytes >> 4, kXChunkStep = C::kChunkBytes >> 4;
+            constexpr uint32_t kAStep = C::kInt8 ? C::kWBytes >> 4 : 64 * C::kStepBlocks;
+            constexpr uint32_t kAChunkStep = C::kInt8 ? block_bytes(FMT) >> 4 : 32;
             const uint32_t x0 = ptx::smem_desc_low(ptx::smem_addr(sm.x(0)));
             const uint32_t a0 = C::kInt8 ? ptx::smem_desc_low(ptx::smem_addr(sm.w(0))) : tmem + C::kACol;
-            constexpr uint32_t kXStep = C::kXBytes >> 4, kAStep = C::kInt8 ? C::kWBytes >> 4 : 64 * C::kABlocks;
-            constexpr uint32_t kXChunkStep = C::kChunkBytes >> 4, kAChunkStep = C::kInt8 ? block_bytes(FMT) >> 4 : 32;
             uint32_t xd = x0, ad = a0;
+            int stage = 0;              // decoded stage (experts)
+            uint32_t a_phase = 0;
             bool ok = true;
             while (ok && walk.next(g)) {
                 ok = wait(sm.d_empty(dr.i), dr.phase ^ 1, &s.abort, kErrAccumulator);
@@ -524,38 +511,33 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                 const uint32_t d = tmem + dr.i * TN;
                 const uint32_t idesc = C::kInt8 ? ptx::idesc_s8(n16) : ptx::idesc_f16(n16);
                 uint32_t add = 0;
-                for (int k = g.k0; ok && k < g.k1; k += C::kABlocks) {
-                    ok = wait(C::kInt8 ? sm.w_full(ar.i) : sm.a_full(ar.i), ar.phase, &s.abort, kErrRing);
-                    const int chunks = (k + C::kABlocks <= g.k1 ? C::kABlocks : g.k1 - k) * C::kChunksPerBlock;
+                for (int k = g.k0; k < g.k1; k += C::kStepBlocks) {
+                    if constexpr (C::kInt8) ok = wait(sm.x_full(r.i), r.phase, &s.abort, kErrRing);
+                    else ok = wait(sm.a_full(stage), a_phase, &s.abort, kErrRing);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const bool full = C::kStepBlocks == 1 || k + 1 < g.k1;
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        if (c < chunks && ok) {
-                            if (c % C::kXChunks == 0) {
-                                ok = wait(sm.x_full(xr.i), xr.phase, &s.abort, kErrRing);
-                                ptx::tc_fence_after();
-                            }
-                            if (ok) {
+                    for (int c = 0; c < C::kChunks; ++c) {
+                        if (c >= C::kChunksPerBlock && !full) break;
+                        const uint32_t a = ad + c * kAChunkStep, b = xd + c * kXChunkStep;
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const uint32_t b = xd + c % C::kXChunks * kXChunkStep + 2 * j;
-                                    const uint32_t more = c == 0 && j == 0 ? add : 1u;
-                                    if constexpr (C::kInt8)
-                                        ptx::mma_s8_ss(d, ad + c * kAChunkStep + 2 * j, b, idesc, more);
-                                    else
-                                        ptx::mma_f16_ts(d, ad + c * kAChunkStep + 8 * j, b, idesc, more);
-                                }
-                            }
-                            if ((c + 1) % C::kXChunks == 0 || c + 1 == chunks) {
-                                ptx::tc_commit(sm.x_empty(xr.i));
-                                xr.step(C::kXStages);
-                                xd = xr.i == 0 ? x0 : xd + kXStep;
-                            }
+                        for (int j = 0; j < 4; ++j) {
+                            if constexpr (C::kInt8) ptx::mma_s8_ss(d, a + 2 * j, b + 2 * j, idesc, c + j ? 1u : add);
+                            else ptx::mma_f16_ts(d, a + 8 * j, b + 2 * j, idesc, c + j ? 1u : add);
                         }
                     }
                     add = 1;
-                    ptx::tc_commit(C::kInt8 ? sm.w_empty(ar.i) : sm.a_empty(ar.i));
-                    ar.step(kAN);
-                    ad = ar.i == 0 ? a0 : ad + kAStep;
+                    ptx::tc_commit(sm.x_empty(r.i));
+                    r.step(C::kXStages);
+                    xd = r.i == 0 ? x0 : xd + kXStep;
+                    if constexpr (C::kInt8) {
+                        ad = r.i == 0 ? a0 : ad + kAStep;
+                    } else {
+                        stage ^= 1;
+                        a_phase ^= stage == 0;
+                        ad = stage == 0 ? a0 : a0 + kAStep;
+                    }
                 }
                 if (!ok) break;
                 ptx::tc_commit(sm.d_full(dr.i));
@@ -563,91 +545,73 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             }
         }
     } else if (warp >= 4 && warp < 4 + C::kDecodeWarps) {
-        // ---- decoders: thread = weight row (warp % 4, lane); the groups take blocks in turn
+        // ---- decoders: thread = weight row (warp % 4, lane); the two groups take steps in turn
         if constexpr (!C::kInt8) {
-            Ring wr;
+            Ring wr, xr, done;      // done: the token slot of this group's last step
             const int row = (warp & 3) * 32 + lane;
-            const int group = (warp - 4) >> 2;      // fills decoded stage `group`, every kGroups-th step
-            const uint32_t dst = tmem + ((uint32_t)(warp & 3) << 21) + C::kACol + group * 64 * C::kABlocks;
-            int turn = group;                       // steps until this group's next
-            uint32_t a_phase = 1;
-            bool ok = true;
+            const int group = (warp - 4) >> 2;      // fills decoded stage `group`
+            const uint32_t dst = tmem + ((uint32_t)(warp & 3) << 21) + C::kACol + group * 64 * C::kStepBlocks;
+            bool turn = group == 0, first = true, ok = true;
             while (ok && walk.next(g)) {
-                for (int k = g.k0; k < g.k1; k += C::kABlocks) {
-                    const int wb = (k - g.k0) % C::kWBlocks;
-                    const bool alone = wb == 0 && k + 1 == g.k1;      // a slot with one block
-                    if (turn == 0) {
-                        turn = C::kGroups - 1;
+                for (int k = g.k0; k < g.k1; k += C::kStepBlocks) {
+                    if (turn) {
+                        // The stage is free when the matrix instructions of the group's last step are
+                        // done; one warp also waits for the tokens, on behalf of the MMA thread.
                         ok = wait(sm.w_full(wr.i), wr.phase, &s.abort, kErrRing);
+                        if (ok && !first) ok = wait(sm.x_empty(done.i), done.phase, &s.abort, kErrRing);
+                        if (ok && (warp & 3) == 0) ok = wait(sm.x_full(xr.i), xr.phase, &s.abort, kErrRing);
                         if (!__all_sync(~0u, ok)) {
                             ok = false;
                             break;
                         }
+                        first = false;
+                        done = xr;
+                        ptx::tc_fence_after();
+                        const uint32_t src = ptx::smem_addr(sm.w(wr.i));
+                        const int halves = C::kStepBlocks == 1 || k + 1 == g.k1 ? 2 : 4;
+                        // not unrolled: the instruction caches hold more of the other roles
+#pragma unroll 1
+                        for (int h = 0; h < halves; ++h) {
+                            const uint32_t blk = src + (h >> 1) * block_bytes(FMT);
+                            uint32_t v[32];
+                            if constexpr (FMT == SKINNY_FMT_NVFP4) {
+                                const uint4 c0 = ptx::lds128(blk + ((h & 1) * 2 * kRows + row) * 16);
+                                const uint4 c1 = ptx::lds128(blk + ((h & 1) * 2 * kRows + kRows + row) * 16);
+                                const uint32_t sc = ptx::lds32(blk + kNvfp4BlockScales + row * 8 + (h & 1) * 4);
+                                uint32_t s01, s23;
+                                ptx::e4m3x4_to_f16x4(sc, s01, s23);
+                                const uint32_t sd[4] = {ptx::dup_lo(s01), ptx::dup_hi(s01), ptx::dup_lo(s23),
+                                                        ptx::dup_hi(s23)};
+                                const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
-                        for (int b = 0; b < C::kABlocks; ++b) {
-                            if (b > 0 && alone) break;
-                            const uint32_t src = ptx::smem_addr(sm.w(wr.i) + (wb + b) * block_bytes(FMT));
-                            constexpr int kWords = FMT == SKINNY_FMT_NVFP4 ? 4 : 8;
-                            uint4 c[kWords];
+                                for (int i = 0; i < 8; ++i) {
+                                    uint32_t f[4];
+                                    ptx::e2m1x8_to_f16x8(words[i], f);
 #pragma unroll
-                            for (int i = 0; i < kWords; ++i) c[i] = ptx::lds128(src + (i * kRows + row) * 16);
-                            uint32_t sc[2] = {0, 0};
-                            if constexpr (FMT == SKINNY_FMT_NVFP4)
-                                ptx::lds64(src + kNvfp4BlockScales + row * 8, sc);
-                            if (b + 1 == C::kABlocks || alone) {
-                                __syncwarp();
-                                if (lane == 0)
-                                    ptx::mbar_arrive_n(sm.w_empty(wr.i), alone ? C::kWBlocks / C::kABlocks : 1);
-                            }
-                            if (b == 0) {
-                                ok = wait(sm.a_empty(group), a_phase, &s.abort, kErrRing);
-                                a_phase ^= 1;
-                                if (!__all_sync(~0u, ok)) {
-                                    ok = false;
-                                    break;
+                                    for (int j = 0; j < 4; ++j) v[4 * i + j] = ptx::hmul2(f[j], sd[i / 2]);
                                 }
-                                ptx::tc_fence_after();
-                            }
+                            } else {
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                uint32_t v[32];
-                                if constexpr (FMT == SKINNY_FMT_NVFP4) {
-                                    uint32_t s01, s23;
-                                    ptx::e4m3x4_to_f16x4(sc[h], s01, s23);
-                                    const uint32_t sd[4] = {ptx::dup_lo(s01), ptx::dup_hi(s01), ptx::dup_lo(s23),
-                                                            ptx::dup_hi(s23)};
-                                    const uint32_t words[8] = {c[2 * h].x,     c[2 * h].y,     c[2 * h].z,
-                                                               c[2 * h].w,     c[2 * h + 1].x, c[2 * h + 1].y,
-                                                               c[2 * h + 1].z, c[2 * h + 1].w};
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) {
-                                        uint32_t f[4];
-                                        ptx::e2m1x8_to_f16x8(words[i], f);
-#pragma unroll
-                                        for (int j = 0; j < 4; ++j) v[4 * i + j] = ptx::hmul2(f[j], sd[i / 2]);
-                                    }
-                                } else {
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const uint4 w = c[4 * h + i];
-                                        ptx::e4m3x4_to_f16x4(w.x, v[8 * i], v[8 * i + 1]);
-                                        ptx::e4m3x4_to_f16x4(w.y, v[8 * i + 2], v[8 * i + 3]);
-                                        ptx::e4m3x4_to_f16x4(w.z, v[8 * i + 4], v[8 * i + 5]);
-                                        ptx::e4m3x4_to_f16x4(w.w, v[8 * i + 6], v[8 * i + 7]);
-                                    }
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint4 w = ptx::lds128(blk + (((h & 1) * 4 + i) * kRows + row) * 16);
+                                    ptx::e4m3x4_to_f16x4(w.x, v[8 * i], v[8 * i + 1]);
+                                    ptx::e4m3x4_to_f16x4(w.y, v[8 * i + 2], v[8 * i + 3]);
+                                    ptx::e4m3x4_to_f16x4(w.z, v[8 * i + 4], v[8 * i + 5]);
+                                    ptx::e4m3x4_to_f16x4(w.w, v[8 * i + 6], v[8 * i + 7]);
                                 }
-                                ptx::tmem_st32(dst + b * 64 + h * 32, v);
                             }
+                            ptx::tmem_st32(dst + h * 32, v);
                         }
-                        if (!ok) break;
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(sm.w_empty(wr.i));
                         ptx::tmem_wait_st();
                         ptx::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(sm.a_full(group));
-                    } else {
-                        --turn;
                     }
-                    if (wb + C::kABlocks == C::kWBlocks || k + C::kABlocks >= g.k1) wr.step(C::kWStages);
+                    turn = !turn;
+                    wr.step(C::kWStages);
+                    xr.step(C::kXStages);
                 }
             }
         }
@@ -780,8 +744,8 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
     if (s.abort && mine) {
         // A wait gave up: copies and matrix instructions may still be in
         // flight.  Let them end before the memory they use is given up.
-        if (warp == 0) drain(r, issued, 1, C::kWStages, sm.w_full(0));
-        if (warp == 1 || (warp == 3 && C::kXProducers == 2)) drain(r, issued, C::kXProducers, C::kXStages, sm.x_full(0));
+        if (warp == 0 && !C::kInt8) drain(r, issued, C::kWStages, sm.w_full(0));
+        if (warp == (C::kInt8 ? 0 : 1)) drain(r, issued, C::kXStages, sm.x_full(0));
         if (warp == 2) {
             ptx::tc_commit(sm.drained());
             ptx::mbar_wait(sm.drained(), 0, kWaitLimitNs);
@@ -923,12 +887,12 @@ int launch(Params p, const void* x, const void* w, int grid, cudaStream_t stream
 {
     using C = Cfg<FMT, TN>;
     CUtensorMap xm, xm2, wm, wm2;
-    if (!make_map(&xm, x, !C::kInt8, p.T, p.K, TN, C::kXChunks)) return SKINNY_ERR_CUDA;
-    if (!make_map(&xm2, x, !C::kInt8, p.T, p.K, C::kX3d ? TN : C::kSmallBox, 1)) return SKINNY_ERR_CUDA;
-    wm = wm2 = xm;
+    if (!make_map(&xm, x, !C::kInt8, p.T, p.K, C::kBox, C::kX3d ? C::kChunks : 1)) return SKINNY_ERR_CUDA;
+    wm = wm2 = xm2 = xm;
+    if (C::kX3d && !make_map(&xm2, x, !C::kInt8, p.T, p.K, C::kBox, 1)) return SKINNY_ERR_CUDA;
     if (C::kInt8) {
-        if (!make_map(&wm, w, false, p.N, p.K, kRows, C::kWBlocks)) return SKINNY_ERR_CUDA;
-        if (C::kWBlocks > 1 && !make_map(&wm2, w, false, p.N, p.K, kRows, 1)) return SKINNY_ERR_CUDA;
+        if (!make_map(&wm, w, false, p.N, p.K, kRows, C::kW3d ? 2 : 1)) return SKINNY_ERR_CUDA;
+        if (C::kW3d && !make_map(&wm2, w, false, p.N, p.K, kRows, 1)) return SKINNY_ERR_CUDA;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
