@@ -96,11 +96,12 @@ struct Cfg {
     static constexpr int kWBytes = block_bytes(FMT) * kStepBlocks;              // a weight slot
     static constexpr int kChunkBytes = TN * 128;
     static constexpr int kXBytes = kChunkBytes * kChunks;                       // a token slot
-    // A narrow tile's tokens arrive in one box per step, a wide one's in boxes
-    // of a quarter of its columns, as many as it has tokens.
+    // A narrow tile's tokens arrive in one box per step, a wide one's in one or
+    // two boxes of half its columns for each chunk, as many as it has tokens (a
+    // box costs the producer ~90 clocks, and a step of a wide tile ~700).
     static constexpr bool kX3d = TN <= 64;
     static constexpr bool kW3d = kInt8 && kStepBlocks == 2;
-    static constexpr int kBox = kX3d ? TN : TN / 4;
+    static constexpr int kBox = kX3d ? TN : TN / 2;
     // Tensor memory: two accumulators at columns 0 and TN, then a stage of
     // decoded blocks, 64 columns a block, for each group of decoder warps.
     static constexpr int kDStages = 2;
@@ -109,6 +110,7 @@ struct Cfg {
     static constexpr int kDecodeWarps = 4 * kGroups;
     static constexpr int kWarps = 4 + kDecodeWarps + 4;
     static constexpr int kThreads = kWarps * 32;
+    static_assert(kInt8 || (kThreads >= kMaxExperts && kWarps <= 32), "make_schedule: a thread per expert");
     // Ring slots.  Experts: weights first, up to what hides HBM's latency (150
     // KB; a wide tile asks for less), and the tokens' ring takes the rest.
     // int8 slots hold weights and tokens.
@@ -135,8 +137,8 @@ struct Cfg {
 struct Schedule {
     int tiles[kMaxExperts + 1];          // running number of tiles
     int rows[kMaxExperts + 1];           // running row offset (offsets made monotone and clamped to [0, T])
-    uint32_t warp_tot_tiles[16];
-    int warp_max[16];
+    uint32_t warp_tot_tiles[32];         // one entry per warp of the block
+    int warp_max[32];
     int total;
     uint32_t tmem;
     int abort;
@@ -273,6 +275,32 @@ __device__ __noinline__ void drain(Ring r, int issued, int stages, uint64_t* ful
     }
 }
 
+// The same for a whole warp, whose lanes leave the wait together: the loop's
+// condition is a vote, so the warp cannot be apart when it comes to the
+// tensor-memory loads and stores, which all lanes must execute as one.
+__device__ __noinline__ bool wait_warp_slow(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned code)
+{
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (__all_sync(~0u, ptx::mbar_try_wait(bar, parity))) return true;
+        if ((i & 31u) == 0) {
+            const uint64_t now = ptx::globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (__any_sync(~0u, now - t0 > kWaitLimitNs)) {
+                *abort = 1;
+                atomicOr(&g_tile_error, code);
+            }
+            if (__any_sync(~0u, *abort != 0)) return false;
+        }
+    }
+}
+
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* abort, unsigned code)
+{
+    if (__all_sync(~0u, ptx::mbar_try_wait(bar, parity))) return true;
+    return wait_warp_slow(bar, parity, abort, code);
+}
+
 template <int FMT, int TN>
 struct Shared {
     using C = Cfg<FMT, TN>;
@@ -312,7 +340,7 @@ __device__ __forceinline__ uint32_t warp_scan_add(uint32_t v)
     return v;
 }
 
-// The experts' schedule, by the whole block (512 threads, one expert each).
+// The experts' schedule, by the whole block (a thread per expert).
 // Offsets are device data that the host has not seen: they are clamped to
 // [0, T] and made non-decreasing, so no row is outside x and y or has two experts.
 template <int TN>
@@ -534,9 +562,11 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                     if constexpr (C::kInt8) {
                         ad = r.i == 0 ? a0 : ad + kAStep;
                     } else {
-                        stage ^= 1;
-                        a_phase ^= stage == 0;
-                        ad = stage == 0 ? a0 : a0 + kAStep;
+                        if (++stage == C::kGroups) {
+                            stage = 0;
+                            a_phase ^= 1;
+                        }
+                        ad = stage == 0 ? a0 : ad + kAStep;
                     }
                 }
                 if (!ok) break;
@@ -551,26 +581,23 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             const int row = (warp & 3) * 32 + lane;
             const int group = (warp - 4) >> 2;      // fills decoded stage `group`
             const uint32_t dst = tmem + ((uint32_t)(warp & 3) << 21) + C::kACol + group * 64 * C::kStepBlocks;
-            bool turn = group == 0, first = true, ok = true;
+            int turn = group;                       // steps until this group's next
+            bool first = true, ok = true;
             while (ok && walk.next(g)) {
                 for (int k = g.k0; k < g.k1; k += C::kStepBlocks) {
-                    if (turn) {
-                        // The stage is free when the matrix instructions of the group's last step are
-                        // done; one warp also waits for the tokens, on behalf of the MMA thread.
-                        ok = wait(sm.w_full(wr.i), wr.phase, &s.abort, kErrRing);
-                        if (ok && !first) ok = wait(sm.x_empty(done.i), done.phase, &s.abort, kErrRing);
-                        if (ok && (warp & 3) == 0) ok = wait(sm.x_full(xr.i), xr.phase, &s.abort, kErrRing);
-                        if (!__all_sync(~0u, ok)) {
-                            ok = false;
-                            break;
-                        }
+                    if (turn == 0) {
+                        turn = C::kGroups;
+                        // the stage is free when the matrix instructions of the group's last step are done
+                        ok = wait_warp(sm.w_full(wr.i), wr.phase, &s.abort, kErrRing);
+                        if (ok && !first) ok = wait_warp(sm.x_empty(done.i), done.phase, &s.abort, kErrRing);
+                        if (!ok) break;
                         first = false;
                         done = xr;
                         ptx::tc_fence_after();
                         const uint32_t src = ptx::smem_addr(sm.w(wr.i));
                         const int halves = C::kStepBlocks == 1 || k + 1 == g.k1 ? 2 : 4;
-                        // not unrolled: the instruction caches hold more of the other roles
-#pragma unroll 1
+                        // not unrolled further: the instruction caches hold more of the other roles
+#pragma unroll 2
                         for (int h = 0; h < halves; ++h) {
                             const uint32_t blk = src + (h >> 1) * block_bytes(FMT);
                             uint32_t v[32];
@@ -606,10 +633,13 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                         if (lane == 0) ptx::mbar_arrive(sm.w_empty(wr.i));
                         ptx::tmem_wait_st();
                         ptx::tc_fence_before();
+                        // one warp waits for the tokens too, on the MMA thread's behalf
+                        if ((warp & 3) == 0) ok = wait_warp(sm.x_full(xr.i), xr.phase, &s.abort, kErrRing);
+                        if (!ok) break;
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(sm.a_full(group));
                     }
-                    turn = !turn;
+                    --turn;
                     wr.step(C::kWStages);
                     xr.step(C::kXStages);
                 }
@@ -623,35 +653,30 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         bool ok = true;
         if (C::kInt8) ptx::pdl_wait_prior_grid();
         while (ok && walk.next(g)) {
-            ok = wait(sm.d_full(dr.i), dr.phase, &s.abort, kErrAccumulator);
-            if (!__all_sync(~0u, ok)) {
-                ok = false;
-                break;
-            }
+            ok = wait_warp(sm.d_full(dr.i), dr.phase, &s.abort, kErrAccumulator);
+            if (!ok) break;
             ptx::tc_fence_after();
             const bool publish = g.k1 < p.C;
             int lowest = blockIdx.x;     // first CTA whose partial sums belong to this tile
             if (!publish && g.k0 > 0) {
                 const int first = g.tile * p.C;
                 while (lowest > 0 && walk.start(lowest) > first) --lowest;
-                // every thread waits for every flag itself: no thread reads a slot it has not acquired
+                // every lane waits for every flag itself: no lane reads a slot it has not acquired
                 const uint64_t t0 = ptx::globaltimer_ns();
                 for (int c = blockIdx.x - 1; ok && c >= lowest; --c) {
                     if (walk.empty(c)) continue;
-                    while ((ptx::ld_acquire_gpu(p.flags + c) & kPublishedMask) != 4) {
-                        if (*(volatile int*)&s.abort) ok = false;
-                        else if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+                    while (!__all_sync(~0u, (ptx::ld_acquire_gpu(p.flags + c) & kPublishedMask) == 4)) {
+                        if (__any_sync(~0u, ptx::globaltimer_ns() - t0 > kWaitLimitNs)) {
                             s.abort = 1;
                             atomicOr(&g_tile_error, kErrPartial);
-                            ok = false;
                         }
-                        if (!ok) break;
+                        if (__any_sync(~0u, *(volatile int*)&s.abort != 0)) {
+                            ok = false;
+                            break;
+                        }
                     }
                 }
-                if (!__all_sync(~0u, ok)) {
-                    ok = false;
-                    break;
-                }
+                if (!ok) break;
             }
             // This thread's channel and scale.  SiLU*mul tiles hold 16 gate
             // rows and their 16 up rows in the two halves of every warp.
