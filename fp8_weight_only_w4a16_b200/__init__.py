@@ -10,9 +10,9 @@ there is no fallback: if the library is missing, the first call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
+import functools
 import os
 import threading
 
@@ -452,21 +452,37 @@ def device_error(clear: bool = True) -> int:
 # Products for any number of tokens: experts and 8-bit integers
 # ---------------------------------------------------------------------------
 
-@contextlib.contextmanager
-def _on(device, *tensors):
-    """Makes `device` current for a call; every tensor must be on it."""
+def _device_of(x, *others) -> int:
+    """The index of x's CUDA device, which every other tensor must be on."""
+    d = x.get_device()
+    if d < 0:
+        raise ValueError("tensors on a CUDA device expected, got %s" % x.device)
+    for t in others:
+        if t is not None and t.get_device() != d:
+            raise ValueError("tensors on one device expected: %s and %s" % (x.device, t.device))
+    return d
+
+
+def _launch(name, d, stream, *args) -> None:
+    """Calls the library's `name` with the stream as its last argument, with device d current."""
     import torch
 
-    if device.type != "cuda":
-        raise ValueError("tensors on a CUDA device expected, got %s" % device)
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("tensors on one device expected: %s and %s" % (device, t.device))
-    if device.index is None or device.index == torch.cuda.current_device():
-        yield
+    fn = getattr(library(), name)
+    if d == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(d) if stream is None else stream.cuda_stream)
     else:
-        with torch.cuda.device(device):
-            yield
+        with torch.cuda.device(d):
+            st = fn(*args, _raw_stream(d) if stream is None else stream.cuda_stream)
+    if st != OK:
+        raise SkinnyError(st, name)
+
+
+def _raw_stream(d: int) -> int:
+    """Handle of the current stream of device d."""
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # without building a Stream object
+    return raw(d) if raw is not None else torch.cuda.current_stream(d).cuda_stream
 
 
 def _ws(workspace):
@@ -475,12 +491,16 @@ def _ws(workspace):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _out_code(y, shape, what):
+def _out_code(y, rows, cols):
     import torch
 
-    if tuple(y.shape) != tuple(shape) or not y.is_contiguous() or y.dtype not in (torch.float16, torch.float32):
-        raise ValueError("%s must be a contiguous float16/float32 %s tensor" % (what, list(shape)))
-    return OUT_F32 if y.dtype == torch.float32 else OUT_F16
+    if y.dim() != 2 or y.shape[0] != rows or y.shape[1] != cols or not y.is_contiguous():
+        raise ValueError("y must be a contiguous float16/float32 [%d, %d] tensor" % (rows, cols))
+    if y.dtype == torch.float16:
+        return OUT_F16
+    if y.dtype == torch.float32:
+        return OUT_F32
+    raise ValueError("y must be a contiguous float16/float32 [%d, %d] tensor" % (rows, cols))
 
 
 def tile_workspace_bytes() -> int:
@@ -495,8 +515,7 @@ def make_experts_workspace(device="cuda"):
     serves calls of any shape in turn, but not two that can run at the same time."""
     import torch
 
-    device = torch.device(device)
-    with _on(device):
+    with torch.cuda.device(device):
         return torch.zeros(tile_workspace_bytes(), dtype=torch.uint8, device=device)
 
 
@@ -511,11 +530,10 @@ def _pack_experts(fmt, codes, scales, E, N, K, gate_up):
     nb = int(library().skinny_experts_packed_bytes(fmt, E, N, K, int(gate_up)))
     if nb == 0:
         raise SkinnyError(ERR_INVALID_ARG, "pack_experts shape")
-    with _on(codes.device, scales):
-        out = torch.empty(nb, dtype=torch.uint8, device=codes.device)
-        st = library().skinny_pack_experts(fmt, codes.data_ptr(), scales.data_ptr() if scales is not None else None,
-                                           E, N, K, int(gate_up), out.data_ptr(), _stream_handle(None))
-        _check(st, "skinny_pack_experts")
+    d = _device_of(codes, scales)
+    out = torch.empty(nb, dtype=torch.uint8, device=codes.device)
+    _launch("skinny_pack_experts", d, None, fmt, codes.data_ptr(), scales.data_ptr() if scales is not None else None,
+            E, N, K, int(gate_up), out.data_ptr())
     return out
 
 
@@ -596,20 +614,17 @@ def _gemm_experts(y, x, w, offsets, workspace, stream, silu):
 
     if w.gate_up != silu:
         raise TypeError("gemm_experts takes experts packed without gate_up, gemm_experts_silu_mul with it")
-    if x.dim() != 2 or x.dtype != torch.float16 or not x.is_contiguous() or x.shape[1] != w.K:
+    if x.dtype != torch.float16 or x.dim() != 2 or x.shape[1] != w.K or not x.is_contiguous():
         raise ValueError("x must be a contiguous float16 [T, %d] tensor" % w.K)
-    if tuple(offsets.shape) != (w.E + 1,) or offsets.dtype != torch.int32 or not offsets.is_contiguous():
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != w.E + 1 or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous int32 [%d] tensor" % (w.E + 1))
     T = x.shape[0]
     outputs = w.N // 2 if silu else w.N
-    out = _out_code(y, (T, outputs), "y")
+    out = _out_code(y, T, outputs)
     ws_ptr, ws_bytes = _ws(workspace)
-    name = "skinny_gemm_experts_silu_mul" if silu else "skinny_gemm_experts"
-    with _on(x.device, y, w.data, w.scale, offsets, workspace):
-        st = getattr(library(), name)(w.fmt, x.data_ptr(), T, w.K, offsets.data_ptr(), w.E, w.data.data_ptr(),
-                                      w.scale.data_ptr(), outputs, y.data_ptr(), out, ws_ptr, ws_bytes,
-                                      _stream_handle(stream))
-    _check(st, name)
+    d = _device_of(x, y, w.data, w.scale, offsets, workspace)
+    _launch("skinny_gemm_experts_silu_mul" if silu else "skinny_gemm_experts", d, stream, w.fmt, x.data_ptr(), T, w.K,
+            offsets.data_ptr(), w.E, w.data.data_ptr(), w.scale.data_ptr(), outputs, y.data_ptr(), out, ws_ptr, ws_bytes)
 
 
 def gemm_experts_into(y, x, w, offsets, workspace=None, stream=None) -> None:
@@ -679,12 +694,10 @@ def quantize_int8_into(q, row_scale, x, stream=None) -> None:
     if q.shape != x.shape or q.dtype != torch.int8 or not q.is_contiguous():
         raise ValueError("q must be a contiguous int8 tensor of x's shape")
     M, K = x.shape
-    if tuple(row_scale.shape) != (M,) or row_scale.dtype != torch.float32 or not row_scale.is_contiguous():
+    if row_scale.dtype != torch.float32 or row_scale.dim() != 1 or row_scale.shape[0] != M or not row_scale.is_contiguous():
         raise ValueError("row_scale must be a contiguous float32 [M] tensor")
-    with _on(x.device, q, row_scale):
-        st = library().skinny_quantize_int8(x.data_ptr(), OUT_F32 if x.dtype == torch.float32 else OUT_F16, M, K,
-                                            q.data_ptr(), row_scale.data_ptr(), _stream_handle(stream))
-    _check(st, "skinny_quantize_int8")
+    _launch("skinny_quantize_int8", _device_of(x, q, row_scale), stream, x.data_ptr(),
+            OUT_F32 if x.dtype == torch.float32 else OUT_F16, M, K, q.data_ptr(), row_scale.data_ptr())
 
 
 def quantize_int8(x, stream=None):
@@ -705,15 +718,13 @@ def gemm_int8_into(y, q, row_scale, w: "WeightInt8", workspace=None, stream=None
     if q.dim() != 2 or q.dtype != torch.int8 or not q.is_contiguous() or q.shape[1] != w.K:
         raise ValueError("q must be a contiguous int8 [M, %d] tensor" % w.K)
     M = q.shape[0]
-    if tuple(row_scale.shape) != (M,) or row_scale.dtype != torch.float32 or not row_scale.is_contiguous():
+    if row_scale.dtype != torch.float32 or row_scale.dim() != 1 or row_scale.shape[0] != M or not row_scale.is_contiguous():
         raise ValueError("row_scale must be a contiguous float32 [M] tensor")
-    out = _out_code(y, (M, w.N), "y")
+    out = _out_code(y, M, w.N)
     ws_ptr, ws_bytes = _ws(workspace)
-    with _on(q.device, y, row_scale, w.codes, w.channel_scale, workspace):
-        st = library().skinny_int8_gemm(q.data_ptr(), row_scale.data_ptr(), M, w.K, w.codes.data_ptr(),
-                                        w.channel_scale.data_ptr(), w.N, y.data_ptr(), out, ws_ptr, ws_bytes,
-                                        _stream_handle(stream))
-    _check(st, "skinny_int8_gemm")
+    _launch("skinny_int8_gemm", _device_of(q, y, row_scale, w.codes, w.channel_scale, workspace), stream, q.data_ptr(),
+            row_scale.data_ptr(), M, w.K, w.codes.data_ptr(), w.channel_scale.data_ptr(), w.N, y.data_ptr(), out, ws_ptr,
+            ws_bytes)
 
 
 def gemm_int8(q, row_scale, w: "WeightInt8", out_dtype=None, workspace=None, stream=None):
@@ -736,6 +747,13 @@ def tile_device_error(clear: bool = True) -> int:
 # Verification of drafted tokens
 # ---------------------------------------------------------------------------
 
+@functools.lru_cache(maxsize=None)
+def _prob_dtypes():
+    import torch
+
+    return {torch.float16: PROB_F16, torch.float32: PROB_F32, torch.bfloat16: PROB_BF16}
+
+
 def verify_draft_into(tokens, accepted, target, draft, draft_tokens, uniform, num_drafts=None, stream=None) -> None:
     """A verify round against the target's probabilities, from given random
     numbers: draft i of a request is accepted while uniform[i] * q_i(d_i) <
@@ -751,8 +769,8 @@ def verify_draft_into(tokens, accepted, target, draft, draft_tokens, uniform, nu
     """
     import torch
 
-    kinds = {torch.float16: PROB_F16, torch.float32: PROB_F32, torch.bfloat16: PROB_BF16}
-    if target.dim() != 3 or target.dtype not in kinds or target.shape[1] < 1 or target.shape[2] < 1:
+    kind = _prob_dtypes().get(target.dtype)
+    if kind is None or target.dim() != 3 or target.shape[1] < 1 or target.shape[2] < 1:
         raise ValueError("target must be a float32/float16/bfloat16 [B, S+1, V] tensor")
     B, S, V = target.shape[0], target.shape[1] - 1, target.shape[2]
     if V > 1 and target.stride(2) != 1:
@@ -768,17 +786,14 @@ def verify_draft_into(tokens, accepted, target, draft, draft_tokens, uniform, nu
                                   (tokens, (B, S + 1), torch.int32, "tokens"), (accepted, (B,), torch.int32, "accepted")):
         if t is None and what == "num_drafts":
             continue
-        if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
             raise ValueError("%s must be a contiguous %s %s tensor" % (what, dtype, list(shape)))
-    with _on(target.device, draft, draft_tokens, uniform, num_drafts, tokens, accepted):
-        has = draft is not None and S > 0
-        st = library().skinny_verify_draft(
-            target.data_ptr(), target.stride(0), target.stride(1), draft.data_ptr() if has else None,
-            draft.stride(0) if has else 0, draft.stride(1) if has else 0, kinds[target.dtype],
+    d = _device_of(target, draft, draft_tokens, uniform, num_drafts, tokens, accepted)
+    has = draft is not None and S > 0
+    _launch("skinny_verify_draft", d, stream, target.data_ptr(), target.stride(0), target.stride(1),
+            draft.data_ptr() if has else None, draft.stride(0) if has else 0, draft.stride(1) if has else 0, kind,
             draft_tokens.data_ptr() if S else None, uniform.data_ptr(),
-            num_drafts.data_ptr() if num_drafts is not None else None, B, S, V, tokens.data_ptr(),
-            accepted.data_ptr(), _stream_handle(stream))
-    _check(st, "skinny_verify_draft")
+            num_drafts.data_ptr() if num_drafts is not None else None, B, S, V, tokens.data_ptr(), accepted.data_ptr())
 
 
 def verify_draft(target, draft, draft_tokens, uniform, num_drafts=None, stream=None):
