@@ -385,6 +385,40 @@ __device__ __forceinline__ void put_column(void* y, int64_t at, int step, const 
     }
 }
 
+// Adds the other CTAs' partial sums of a tile (slots of CTAs blockIdx.x - 1
+// down to `lowest`) to this warp's rows of the accumulator, SLOTS slots and
+// COLS columns at a time.
+template <bool INT8, int SLOTS, int COLS, int TN>
+__device__ __forceinline__ void add_partials(const Params& p, const Walk<TN>& walk, int lowest, int row, int n,
+                                             uint32_t acc)
+{
+#pragma unroll 1
+    for (int c0 = 0; c0 < n; c0 += COLS) {
+        uint32_t v[COLS];
+        ptx::tmem_ld(acc + c0, v);
+        const int left = n - c0;
+#pragma unroll 1
+        for (int c = blockIdx.x - 1; c >= lowest; c -= SLOTS) {
+            uint32_t part[SLOTS][COLS];
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i) {
+                const bool there = c - i >= lowest && !walk.empty(c - i);
+                const unsigned* slot = p.partials + (int64_t)(c - i) * kSlotWords + row + c0 * kRows;
+#pragma unroll
+                for (int j = 0; j < COLS; ++j) part[i][j] = there && j < left ? __ldcg(slot + j * kRows) : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < SLOTS; ++i)
+#pragma unroll
+                for (int j = 0; j < COLS; ++j)
+                    v[j] = INT8 ? v[j] + part[i][j]
+                                : __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(part[i][j]));
+        }
+        ptx::tmem_st(acc + c0, v);
+    }
+    ptx::tmem_wait_st();
+}
+
 template <int FMT, int TN, bool SILU>
 __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
     tile_gemm(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap x_map,
@@ -627,7 +661,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                                     ptx::e4m3x4_to_f16x4(w.w, v[8 * i + 6], v[8 * i + 7]);
                                 }
                             }
-                            ptx::tmem_st32(dst + h * 32, v);
+                            ptx::tmem_st(dst + h * 32, v);
                         }
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(sm.w_empty(wr.i));
@@ -653,10 +687,22 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         bool ok = true;
         if (C::kInt8) ptx::pdl_wait_prior_grid();
         while (ok && walk.next(g)) {
+            const bool publish = g.k1 < p.C;
+            // This thread's channel and scale.  SiLU*mul tiles hold 16 gate
+            // rows and their 16 up rows in the two halves of every warp.
+            const int o = SILU ? g.row_tile * 64 + q * 16 + (lane & 15) : g.row_tile * kRows + row;
+            const bool valid = o < p.outputs;
+            float scale = 0.f, rs = 0.f;      // loaded while the tile is computed
+            if (valid && !publish) {
+                if (FMT == SKINNY_FMT_NVFP4) scale = p.scale[g.e];
+                else if (FMT == SKINNY_FMT_FP8)
+                    scale = p.scale[(size_t)g.e * p.N + o + (SILU && lane >= 16 ? p.outputs : 0)];
+                else scale = p.scale[o];
+            }
+            if (C::kInt8 && !publish && lane < g.n) rs = p.row_scale[g.t0 + lane];
             ok = wait_warp(sm.d_full(dr.i), dr.phase, &s.abort, kErrAccumulator);
             if (!ok) break;
             ptx::tc_fence_after();
-            const bool publish = g.k1 < p.C;
             int lowest = blockIdx.x;     // first CTA whose partial sums belong to this tile
             if (!publish && g.k0 > 0) {
                 const int first = g.tile * p.C;
@@ -678,72 +724,53 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                 }
                 if (!ok) break;
             }
-            // This thread's channel and scale.  SiLU*mul tiles hold 16 gate
-            // rows and their 16 up rows in the two halves of every warp.
-            const int o = SILU ? g.row_tile * 64 + q * 16 + (lane & 15) : g.row_tile * kRows + row;
-            const bool valid = o < p.outputs;
-            float scale = 0.f;
-            if (valid && !publish) {
-                if (FMT == SKINNY_FMT_NVFP4) scale = p.scale[g.e];
-                else if (FMT == SKINNY_FMT_FP8)
-                    scale = p.scale[(size_t)g.e * p.N + o + (SILU && lane >= 16 ? p.outputs : 0)];
-                else scale = p.scale[o];
+            const uint32_t acc = src + dr.i * TN;
+            // Other CTAs' sums are added to the accumulator, from the nearest CTA down (a fixed
+            // order), with 32 loads in flight per thread: four CTAs' for few tokens, else 32 tokens'.
+            if (lowest < (int)blockIdx.x) {
+                if (g.n <= 8) add_partials<C::kInt8, 4, 8>(p, walk, lowest, row, g.n, acc);
+                else if (TN > 16) add_partials<C::kInt8, 1, 32>(p, walk, lowest, row, g.n, acc);
+                else add_partials<C::kInt8, 4, 8>(p, walk, lowest, row, g.n, acc);
             }
-            for (int c0 = 0; c0 < g.n; c0 += 32) {
-                // Everything loaded here is loaded before the first store: the
-                // compiler cannot move a load across one.
-                float rs = 0.f;
-                if (C::kInt8 && !publish && c0 + lane < g.n) rs = p.row_scale[g.t0 + c0 + lane];
-                uint32_t v[32];
-                if constexpr (TN == 16) {
-                    uint32_t lo[16];
-                    ptx::tmem_ld16(src + dr.i * TN + c0, lo);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = j < 16 ? lo[j] : 0;
-                } else {
-                    ptx::tmem_ld32(src + dr.i * TN + c0, v);
-                }
+            // Narrow tiles go by eight columns at a time: the loop's code is short (a first pass
+            // through it comes from memory) and one token costs one turn.
+            constexpr int kCols = TN <= 64 ? 8 : 32;
+#pragma unroll 1
+            for (int c0 = 0; c0 < g.n; c0 += kCols) {
+                if (C::kInt8 && !publish && c0 > 0 && c0 % 32 == 0)
+                    rs = c0 + lane < g.n ? p.row_scale[g.t0 + c0 + lane] : 0.f;
+                uint32_t v[kCols];
+                ptx::tmem_ld(acc + c0, v);
                 const int left = g.n - c0;
                 if (publish) {
                     unsigned* slot = p.partials + (size_t)blockIdx.x * kSlotWords + row + c0 * kRows;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < kCols; ++j)
                         if (j < left) slot[j * kRows] = v[j];
                     continue;
-                }
-                for (int c = blockIdx.x - 1; c >= lowest; --c) {
-                    if (walk.empty(c)) continue;
-                    const unsigned* slot = p.partials + (size_t)c * kSlotWords + row + c0 * kRows;
-                    uint32_t o32[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) o32[j] = j < left ? __ldcg(slot + j * kRows) : 0;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = C::kInt8 ? v[j] + o32[j]
-                                        : __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(o32[j]));
                 }
                 // y of this thread's channel at the chunk's first token
                 const int64_t at = (int64_t)(g.t0 + c0) * p.outputs + o;
                 if constexpr (SILU) {
-                    float r[16];
+                    float r[kCols / 2];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
+                    for (int j = 0; j < kCols; j += 2) {
                         // lanes 0..15 finish token j, lanes 16..31 token j + 1
                         const float a = __uint_as_float(v[j]) * scale, b = __uint_as_float(v[j + 1]) * scale;
                         const float other = __shfl_xor_sync(~0u, lane < 16 ? b : a, 16);
                         const float gate = lane < 16 ? a : other, up = lane < 16 ? other : b;
                         r[j / 2] = gate / (1.f + expf(-gate)) * up;
                     }
-                    put_column<16>(p.y, at + (lane >> 4) * p.outputs, 2 * p.outputs, r,
-                                   valid ? (left + 1 - (lane >> 4)) / 2 : 0, p.out_f32);
+                    put_column<kCols / 2>(p.y, at + (lane >> 4) * p.outputs, 2 * p.outputs, r,
+                                          valid ? (left + 1 - (lane >> 4)) / 2 : 0, p.out_f32);
                 } else {
-                    float r[32];
+                    float r[kCols];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if constexpr (C::kInt8) r[j] = (float)(int)v[j] * __shfl_sync(~0u, rs, j) * scale;
+                    for (int j = 0; j < kCols; ++j) {
+                        if constexpr (C::kInt8) r[j] = (float)(int)v[j] * __shfl_sync(~0u, rs, c0 % 32 + j) * scale;
                         else r[j] = __uint_as_float(v[j]) * scale;
                     }
-                    put_column<32>(p.y, at, p.outputs, r, valid ? left : 0, p.out_f32);
+                    put_column<kCols>(p.y, at, p.outputs, r, valid ? left : 0, p.out_f32);
                 }
             }
             ptx::tc_fence_before();
