@@ -90,18 +90,24 @@ constexpr int at_most(int a, int b) { return a < b ? a : b; }
 template <int FMT, int TN>
 struct Cfg {
     static constexpr bool kInt8 = FMT == kFmtInt8;
-    static constexpr int kStepBlocks = TN > 64 ? 1 : 2;
+    // Wide tiles are computed by pairs of CTAs (a cluster): 256 weight rows, 128
+    // in each CTA, and half the tokens' rows loaded by each.  One CTA by itself
+    // would read 96 bytes (experts: 80) from L2 per clock of matrix instructions,
+    // where an SM gets about 64.
+    static constexpr bool kPair = TN > 64;
+    static constexpr int kStepBlocks = kPair ? 1 : 2;
+    static constexpr int kTokens = kPair ? TN / 2 : TN;                         // tokens in this CTA's slots
     static constexpr int kChunksPerBlock = kInt8 ? 1 : 2;                       // 128-byte wide pieces of x per block
     static constexpr int kChunks = kStepBlocks * kChunksPerBlock;               // pieces per step
     static constexpr int kWBytes = block_bytes(FMT) * kStepBlocks;              // a weight slot
-    static constexpr int kChunkBytes = TN * 128;
+    static constexpr int kChunkBytes = kTokens * 128;
     static constexpr int kXBytes = kChunkBytes * kChunks;                       // a token slot
     // A narrow tile's tokens arrive in one box per step, a wide one's in one or
-    // two boxes of half its columns for each chunk, as many as it has tokens (a
-    // box costs the producer ~90 clocks, and a step of a wide tile ~700).
-    static constexpr bool kX3d = TN <= 64;
+    // two boxes for each chunk, as many as it has tokens (a box costs the
+    // producer ~90 clocks, a step of a wide tile takes 500 to 700).
+    static constexpr bool kX3d = !kPair;
     static constexpr bool kW3d = kInt8 && kStepBlocks == 2;
-    static constexpr int kBox = kX3d ? TN : TN / 2;
+    static constexpr int kBox = kX3d ? TN : kTokens / 2;
     // Tensor memory: two accumulators at columns 0 and TN, then a stage of
     // decoded blocks, 64 columns a block, for each group of decoder warps.
     static constexpr int kDStages = 2;
@@ -115,7 +121,7 @@ struct Cfg {
     // KB; a wide tile asks for less), and the tokens' ring takes the rest.
     // int8 slots hold weights and tokens.
     static constexpr int kBudget = 218 * 1024;
-    static constexpr int kWTarget = (TN > 64 ? 72 : 150) * 1024;
+    static constexpr int kWTarget = (kPair ? 96 : 150) * 1024;
     static constexpr int kWStages = kInt8 ? at_most(kBudget / (kWBytes + kXBytes), 12)
                                           : at_most((kBudget - 3 * kXBytes) / kWBytes, kWTarget / kWBytes);
     static constexpr int kXStages = kInt8 ? kWStages : at_most((kBudget - kWStages * kWBytes) / kXBytes, 12);
@@ -147,6 +153,13 @@ struct Schedule {
 __device__ __forceinline__ int token_tiles(int rows, int TN) { return (rows + TN - 1) / TN; }
 __device__ __forceinline__ int tile_rows(int rows, int nt) { return ((rows + nt - 1) / nt + 15) & ~15; }
 
+// What a tile has of the weight's row tiles: one, or a pair's two.
+template <bool PAIR>
+__device__ __forceinline__ int row_groups(const Params& p)
+{
+    return PAIR ? (p.G + 1) / 2 : p.G;
+}
+
 // Largest e with a[e] <= v, 0 <= e < n (a[0] = 0, a ascending).
 __device__ __forceinline__ int find(const int* a, int n, int v)
 {
@@ -161,32 +174,38 @@ __device__ __forceinline__ int find(const int* a, int n, int v)
 
 // A piece of one CTA's work: K blocks [k0, k1) of a tile.
 struct Segment {
-    int e, row_tile, t0, n;   // expert, row tile, first token row, token rows
+    int e, row_tile, t0, n;   // expert, this CTA's row tile, first token row, token rows
     int tile, k0, k1;
 };
 
 // The CTA's pieces.  Whole tiles are dealt out one after another, so that the
 // CTAs work on neighbouring tiles and share their operands in L2.  What would
 // leave CTAs idle in the last round is split along K instead: the first
-// `splits` tiles (all, if there are fewer than two per CTA; otherwise the
-// remainder and one round) are cut into equal contiguous ranges of blocks,
-// one per CTA, and the partial sums of a cut tile meet in the workspace.  A
-// range is walked backwards, so that the sums another CTA waits for come first.
-template <int TN>
+// `splits` tiles (the remainder, and one round more where the remainder is
+// less than a quarter of a round, which would leave many CTAs on one tile) are
+// cut into equal contiguous ranges of blocks, one per CTA, and the partial
+// sums of a cut tile meet in the workspace.  They come first, so that the
+// exchange is hidden behind the whole tiles, and a range is walked backwards,
+// so that the sums another CTA waits for come first of all.
+// A pair of CTAs counts as one here.
+template <int TN, bool PAIR>
 struct Walk {
     const Schedule& s;
     const Params& p;
+    int P, self;        // CTAs (or pairs) of the grid, and which this is
     int share, extra;   // split blocks: CTA b has share + (b < extra)
     int u0, u;          // this CTA's first block, and one past the next piece's last
     int tile;           // the next whole tile
 
     __device__ Walk(const Schedule& s_, const Params& p_) : s(s_), p(p_)
     {
-        const int P = gridDim.x, b = blockIdx.x;
+        P = PAIR ? gridDim.x / 2 : gridDim.x;
+        self = PAIR ? blockIdx.x / 2 : blockIdx.x;
+        const int b = self;
         int splits = 0;
         if (p.partials != nullptr) {
-            if (s.total < 2 * P) splits = s.total;
-            else if (const int rest = s.total % P; rest != 0) splits = rest + P;
+            const int rest = s.total % P;
+            splits = rest == 0 || 4 * rest >= P ? rest : s.total < P ? rest : rest + P;
         }
         share = splits * p.C / P;
         extra = splits * p.C % P;
@@ -195,6 +214,8 @@ struct Walk {
         tile = splits + b;
     }
     __device__ int start(int b) const { return b * share + (b < extra ? b : extra); }
+    // the workspace slot that this CTA reads of CTA (or pair) b
+    __device__ int slot(int b) const { return PAIR ? 2 * b + (int)(blockIdx.x & 1) : b; }
     __device__ bool empty(int b) const { return share == 0 && b >= extra; }
     __device__ bool next(Segment& g)
     {
@@ -208,14 +229,15 @@ struct Walk {
             g.tile = tile;
             g.k0 = 0;
             g.k1 = p.C;
-            tile += gridDim.x;
+            tile += P;
         }
         g.e = find(s.tiles, p.E, g.tile);
         const int m = s.rows[g.e + 1] - s.rows[g.e];
         const int q = tile_rows(m, token_tiles(m, TN));
         const int lt = g.tile - s.tiles[g.e];
-        g.row_tile = lt % p.G;
-        const int t = lt / p.G * q;
+        const int groups = row_groups<PAIR>(p);
+        g.row_tile = PAIR ? lt % groups * 2 + (int)(blockIdx.x & 1) : lt % groups;
+        const int t = lt / groups * q;
         g.t0 = s.rows[g.e] + t;
         g.n = m - t < q ? m - t : q;
         return true;
@@ -343,7 +365,7 @@ __device__ __forceinline__ uint32_t warp_scan_add(uint32_t v)
 // The experts' schedule, by the whole block (a thread per expert).
 // Offsets are device data that the host has not seen: they are clamped to
 // [0, T] and made non-decreasing, so no row is outside x and y or has two experts.
-template <int TN>
+template <int TN, bool PAIR>
 __device__ void make_schedule(Schedule& s, const Params& p)
 {
     const int i = threadIdx.x, w = i / 32;
@@ -358,7 +380,7 @@ __device__ void make_schedule(Schedule& s, const Params& p)
     if (i == 0) s.rows[0] = first;
     if (i < p.E) s.rows[i + 1] = v;
     __syncthreads();
-    uint32_t n = i < p.E ? (uint32_t)token_tiles(s.rows[i + 1] - s.rows[i], TN) * (uint32_t)p.G : 0;
+    uint32_t n = i < p.E ? (uint32_t)token_tiles(s.rows[i + 1] - s.rows[i], TN) * (uint32_t)row_groups<PAIR>(p) : 0;
     n = warp_scan_add(n);
     if ((i & 31) == 31) s.warp_tot_tiles[w] = n;
     __syncthreads();
@@ -385,11 +407,49 @@ __device__ __forceinline__ void put_column(void* y, int64_t at, int step, const 
     }
 }
 
-// Adds the other CTAs' partial sums of a tile (slots of CTAs blockIdx.x - 1
+// One row's 128 columns of a packed block (shared-memory address `src`) to
+// FP16, two to a word, in two halves.
+template <int FMT>
+__device__ __forceinline__ void decode(uint32_t src, int row, uint32_t (&v)[2][32])
+{
+    if constexpr (FMT == SKINNY_FMT_NVFP4) {
+        uint32_t sc[2];
+        ptx::lds64(src + kNvfp4BlockScales + row * 8, sc);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 c0 = ptx::lds128(src + (2 * h * kRows + row) * 16);
+            const uint4 c1 = ptx::lds128(src + ((2 * h + 1) * kRows + row) * 16);
+            uint32_t s01, s23;
+            ptx::e4m3x4_to_f16x4(sc[h], s01, s23);
+            const uint32_t sd[4] = {ptx::dup_lo(s01), ptx::dup_hi(s01), ptx::dup_lo(s23), ptx::dup_hi(s23)};
+            const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t f[4];
+                ptx::e2m1x8_to_f16x8(words[i], f);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[h][4 * i + j] = ptx::hmul2(f[j], sd[i / 2]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 w = ptx::lds128(src + ((4 * h + i) * kRows + row) * 16);
+                ptx::e4m3x4_to_f16x4(w.x, v[h][8 * i], v[h][8 * i + 1]);
+                ptx::e4m3x4_to_f16x4(w.y, v[h][8 * i + 2], v[h][8 * i + 3]);
+                ptx::e4m3x4_to_f16x4(w.z, v[h][8 * i + 4], v[h][8 * i + 5]);
+                ptx::e4m3x4_to_f16x4(w.w, v[h][8 * i + 6], v[h][8 * i + 7]);
+            }
+    }
+}
+
+// Adds the other CTAs' partial sums of a tile (slots of CTAs or pairs self - 1
 // down to `lowest`) to this warp's rows of the accumulator, SLOTS slots and
 // COLS columns at a time.
-template <bool INT8, int SLOTS, int COLS, int TN>
-__device__ __forceinline__ void add_partials(const Params& p, const Walk<TN>& walk, int lowest, int row, int n,
+template <bool INT8, int SLOTS, int COLS, int TN, bool PAIR>
+__device__ __forceinline__ void add_partials(const Params& p, const Walk<TN, PAIR>& walk, int lowest, int row, int n,
                                              uint32_t acc)
 {
 #pragma unroll 1
@@ -398,12 +458,12 @@ __device__ __forceinline__ void add_partials(const Params& p, const Walk<TN>& wa
         ptx::tmem_ld(acc + c0, v);
         const int left = n - c0;
 #pragma unroll 1
-        for (int c = blockIdx.x - 1; c >= lowest; c -= SLOTS) {
+        for (int c = walk.self - 1; c >= lowest; c -= SLOTS) {
             uint32_t part[SLOTS][COLS];
 #pragma unroll
             for (int i = 0; i < SLOTS; ++i) {
                 const bool there = c - i >= lowest && !walk.empty(c - i);
-                const unsigned* slot = p.partials + (int64_t)(c - i) * kSlotWords + row + c0 * kRows;
+                const unsigned* slot = p.partials + (int64_t)walk.slot(c - i) * kSlotWords + row + c0 * kRows;
 #pragma unroll
                 for (int j = 0; j < COLS; ++j) part[i][j] = there && j < left ? __ldcg(slot + j * kRows) : 0;
             }
@@ -433,17 +493,17 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kXStages; ++i) {
-            ptx::mbar_init(sm.x_full(i), C::kInt8 ? 2 : 1);      // int8: both producers' copies
+            ptx::mbar_init(sm.x_full(i), C::kInt8 && !C::kPair ? 2 : 1);      // int8: both producers' copies
             ptx::mbar_init(sm.x_empty(i), 1);
         }
         for (int i = 0; i < C::kWStages; ++i) {
             ptx::mbar_init(sm.w_full(i), 1);
             ptx::mbar_init(sm.w_empty(i), 4);
         }
-        for (int i = 0; i < C::kGroups; ++i) ptx::mbar_init(sm.a_full(i), 4);
+        for (int i = 0; i < C::kGroups; ++i) ptx::mbar_init(sm.a_full(i), C::kPair ? 8 : 4);
         for (int i = 0; i < C::kDStages; ++i) {
             ptx::mbar_init(sm.d_full(i), 1);
-            ptx::mbar_init(sm.d_empty(i), 4);
+            ptx::mbar_init(sm.d_empty(i), C::kPair ? 8 : 4);
         }
         ptx::mbar_init(sm.drained(), 1);
         ptx::fence_mbar_init();
@@ -452,7 +512,9 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         if (C::kInt8) ptx::prefetch_tensormap(&w_map);
         s.abort = 0;
     }
-    if (warp == 2) ptx::tmem_alloc_all(&s.tmem);
+    if (warp == 2) ptx::tmem_alloc_all<C::kPair>(&s.tmem);
+    const int rank = C::kPair ? (int)ptx::cluster_rank() : 0;
+    const bool leader = rank == 0;
     ptx::pdl_launch_dependents();
     if constexpr (C::kInt8) {
         // The schedule needs nothing of the previous kernel: only the roles
@@ -461,17 +523,18 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             s.rows[0] = 0;
             s.rows[1] = p.T;
             s.tiles[0] = 0;
-            s.tiles[1] = s.total = token_tiles(p.T, TN) * p.G;
+            s.tiles[1] = s.total = token_tiles(p.T, TN) * row_groups<C::kPair>(p);
         }
     } else {
         ptx::pdl_wait_prior_grid();
-        make_schedule<TN>(s, p);
+        make_schedule<TN, C::kPair>(s, p);
     }
     ptx::tc_fence_before();
     __syncthreads();
+    if constexpr (C::kPair) ptx::cluster_sync();      // the other CTA's barriers are ready, too
     ptx::tc_fence_after();
     const uint32_t tmem = s.tmem;
-    Walk<TN> walk(s, p);
+    Walk<TN, C::kPair> walk(s, p);
     Segment g;
     Ring r;            // position of a single-thread role, and how much it has issued
     int issued = 0;
@@ -487,13 +550,25 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             bool ok = true;
             const uint64_t pol = TN <= 32 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
             while (ok && walk.next(g)) {
-                const uint8_t* src =
-                    C::kInt8 ? nullptr : p.w + ((size_t)g.e * p.G + g.row_tile) * p.C * block_bytes(FMT);
+                // (an odd last row tile has no partner: its pair's second CTA computes it too, and stores nothing)
+                const int rt = C::kPair && g.row_tile >= p.G ? p.G - 1 : g.row_tile;
+                const uint8_t* src = C::kInt8 ? nullptr : p.w + ((size_t)g.e * p.G + rt) * p.C * block_bytes(FMT);
+                const uint32_t pair_bytes =
+                    2 * (C::kWBytes + (((g.n + 15) & ~15) / 2 + C::kBox - 1) / C::kBox * C::kBox * 128);
                 for (int k = g.k0; k < g.k1; k += C::kStepBlocks) {
                     ok = wait(C::kInt8 ? sm.x_empty(r.i) : sm.w_empty(r.i), r.phase ^ 1, &s.abort, kErrRing);
                     if (!ok) break;
                     if constexpr (C::kInt8) {
                         uint64_t* full = sm.x_full(r.i);
+                        if constexpr (C::kPair) {
+                            // the leader's barrier counts both CTAs' weights and tokens
+                            if (leader) ptx::mbar_arrive_expect_tx(full, pair_bytes);
+                            ptx::tma_load_2d_pair(sm.w(r.i), &w_map, k * kBlockK, rt * kRows, ptx::leader_addr(full),
+                                                  pol);
+                            r.step(C::kWStages);
+                            ++issued;
+                            continue;
+                        }
                         ptx::mbar_arrive_expect_tx(full, C::kWBytes);
                         if (C::kW3d && (k + 2) * kBlockK <= p.K) {
                             ptx::tma_load_3d(sm.w(r.i), &w_map, 0, g.row_tile * kRows, k, full, pol);
@@ -524,7 +599,9 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             const int whole = p.K / kChunkK;      // pieces that lie within K entirely
             while (ok && walk.next(g)) {
                 const int c1 = g.k1 * C::kChunksPerBlock;
-                const int boxes = (g.n + C::kBox - 1) / C::kBox;
+                // a pair's CTA has half the tile's columns
+                const int half = ((g.n + 15) & ~15) / 2, first = g.t0 + rank * half;
+                const int boxes = (half + C::kBox - 1) / C::kBox;
                 for (int c = g.k0 * C::kChunksPerBlock; c < c1; c += C::kChunks) {
                     ok = wait(sm.x_empty(r.i), r.phase ^ 1, &s.abort, kErrRing);
                     if (!ok) break;
@@ -541,11 +618,16 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                                                  sm.x_full(r.i), pol);
                         }
                     } else {
-                        ptx::mbar_arrive_expect_tx(sm.x_full(r.i), C::kChunks * boxes * C::kBox * 128);
+                        if (!C::kInt8)
+                            ptx::mbar_arrive_expect_tx(sm.x_full(r.i), C::kChunks * boxes * C::kBox * 128);
                         for (int h = 0; h < C::kChunks; ++h)
-                            for (int b = 0; b < boxes; ++b)
-                                ptx::tma_load_2d(sm.x(r.i) + h * C::kChunkBytes + b * C::kBox * 128, &x_map,
-                                                 (c + h) * kChunkK, g.t0 + b * C::kBox, sm.x_full(r.i), pol);
+                            for (int b = 0; b < boxes; ++b) {
+                                uint8_t* dst = sm.x(r.i) + h * C::kChunkBytes + b * C::kBox * 128;
+                                const int col = (c + h) * kChunkK, at = first + b * C::kBox;
+                                if constexpr (C::kInt8)
+                                    ptx::tma_load_2d_pair(dst, &x_map, col, at, ptx::leader_addr(sm.x_full(r.i)), pol);
+                                else ptx::tma_load_2d(dst, &x_map, col, at, sm.x_full(r.i), pol);
+                            }
                     }
                     r.step(C::kXStages);
                     ++issued;
@@ -553,8 +635,8 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             }
         }
     } else if (warp == 2) {
-        // ---- MMA: one thread issues
-        if (ptx::elect_one()) {
+        // ---- MMA: one thread issues (a pair's: the leader's)
+        if (leader && ptx::elect_one()) {
             mine = true;
             Ring dr;
             constexpr uint32_t kXStep = C::kXBytes >> 4, kXChunkStep = C::kChunkBytes >> 4;
@@ -571,7 +653,8 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                 if (!ok) break;
                 const int n16 = (g.n + 15) & ~15;
                 const uint32_t d = tmem + dr.i * TN;
-                const uint32_t idesc = C::kInt8 ? ptx::idesc_s8(n16) : ptx::idesc_f16(n16);
+                constexpr int kM = C::kPair ? 2 * kRows : kRows;
+                const uint32_t idesc = C::kInt8 ? ptx::idesc_s8(kM, n16) : ptx::idesc_f16(kM, n16);
                 uint32_t add = 0;
                 for (int k = g.k0; k < g.k1; k += C::kStepBlocks) {
                     if constexpr (C::kInt8) ok = wait(sm.x_full(r.i), r.phase, &s.abort, kErrRing);
@@ -585,12 +668,12 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                         const uint32_t a = ad + c * kAChunkStep, b = xd + c * kXChunkStep;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            if constexpr (C::kInt8) ptx::mma_s8_ss(d, a + 2 * j, b + 2 * j, idesc, c + j ? 1u : add);
-                            else ptx::mma_f16_ts(d, a + 8 * j, b + 2 * j, idesc, c + j ? 1u : add);
+                            if constexpr (C::kInt8) ptx::mma_s8_ss<C::kPair>(d, a + 2 * j, b + 2 * j, idesc, c + j ? 1u : add);
+                            else ptx::mma_f16_ts<C::kPair>(d, a + 8 * j, b + 2 * j, idesc, c + j ? 1u : add);
                         }
                     }
                     add = 1;
-                    ptx::tc_commit(sm.x_empty(r.i));
+                    ptx::tc_commit<C::kPair>(sm.x_empty(r.i));
                     r.step(C::kXStages);
                     xd = r.i == 0 ? x0 : xd + kXStep;
                     if constexpr (C::kInt8) {
@@ -604,7 +687,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                     }
                 }
                 if (!ok) break;
-                ptx::tc_commit(sm.d_full(dr.i));
+                ptx::tc_commit<C::kPair>(sm.d_full(dr.i));
                 dr.step(C::kDStages);
             }
         }
@@ -621,48 +704,28 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                 for (int k = g.k0; k < g.k1; k += C::kStepBlocks) {
                     if (turn == 0) {
                         turn = C::kGroups;
-                        // the stage is free when the matrix instructions of the group's last step are done
                         ok = wait_warp(sm.w_full(wr.i), wr.phase, &s.abort, kErrRing);
-                        if (ok && !first) ok = wait_warp(sm.x_empty(done.i), done.phase, &s.abort, kErrRing);
+                        if (!ok) break;
+                        const uint32_t src = ptx::smem_addr(sm.w(wr.i));
+                        const int blocks = C::kStepBlocks == 1 || k + 1 == g.k1 ? 1 : 2;
+                        // one copy of the code for both blocks: the instruction caches hold more of the other roles
+#pragma unroll 1
+                        for (int b = 0; b < blocks; ++b) {
+                            uint32_t v[2][32];
+                            decode<FMT>(src + b * block_bytes(FMT), row, v);
+                            if (b == 0 && !first) {
+                                // the stage is free when the matrix instructions of the group's last step
+                                // are done: the conversion does not wait for them
+                                ok = wait_warp(sm.x_empty(done.i), done.phase, &s.abort, kErrRing);
+                                if (!ok) break;
+                            }
+                            ptx::tc_fence_after();
+                            ptx::tmem_st(dst + b * 64, v[0]);
+                            ptx::tmem_st(dst + b * 64 + 32, v[1]);
+                        }
                         if (!ok) break;
                         first = false;
                         done = xr;
-                        ptx::tc_fence_after();
-                        const uint32_t src = ptx::smem_addr(sm.w(wr.i));
-                        const int halves = C::kStepBlocks == 1 || k + 1 == g.k1 ? 2 : 4;
-                        // not unrolled further: the instruction caches hold more of the other roles
-#pragma unroll 2
-                        for (int h = 0; h < halves; ++h) {
-                            const uint32_t blk = src + (h >> 1) * block_bytes(FMT);
-                            uint32_t v[32];
-                            if constexpr (FMT == SKINNY_FMT_NVFP4) {
-                                const uint4 c0 = ptx::lds128(blk + ((h & 1) * 2 * kRows + row) * 16);
-                                const uint4 c1 = ptx::lds128(blk + ((h & 1) * 2 * kRows + kRows + row) * 16);
-                                const uint32_t sc = ptx::lds32(blk + kNvfp4BlockScales + row * 8 + (h & 1) * 4);
-                                uint32_t s01, s23;
-                                ptx::e4m3x4_to_f16x4(sc, s01, s23);
-                                const uint32_t sd[4] = {ptx::dup_lo(s01), ptx::dup_hi(s01), ptx::dup_lo(s23),
-                                                        ptx::dup_hi(s23)};
-                                const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    uint32_t f[4];
-                                    ptx::e2m1x8_to_f16x8(words[i], f);
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j) v[4 * i + j] = ptx::hmul2(f[j], sd[i / 2]);
-                                }
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const uint4 w = ptx::lds128(blk + (((h & 1) * 4 + i) * kRows + row) * 16);
-                                    ptx::e4m3x4_to_f16x4(w.x, v[8 * i], v[8 * i + 1]);
-                                    ptx::e4m3x4_to_f16x4(w.y, v[8 * i + 2], v[8 * i + 3]);
-                                    ptx::e4m3x4_to_f16x4(w.z, v[8 * i + 4], v[8 * i + 5]);
-                                    ptx::e4m3x4_to_f16x4(w.w, v[8 * i + 6], v[8 * i + 7]);
-                                }
-                            }
-                            ptx::tmem_st(dst + h * 32, v);
-                        }
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive(sm.w_empty(wr.i));
                         ptx::tmem_wait_st();
@@ -671,7 +734,10 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                         if ((warp & 3) == 0) ok = wait_warp(sm.x_full(xr.i), xr.phase, &s.abort, kErrRing);
                         if (!ok) break;
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(sm.a_full(group));
+                        if (lane == 0) {
+                            if constexpr (C::kPair) ptx::mbar_arrive_leader(sm.a_full(group));
+                            else ptx::mbar_arrive(sm.a_full(group));
+                        }
                     }
                     --turn;
                     wr.step(C::kWStages);
@@ -703,15 +769,15 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             ok = wait_warp(sm.d_full(dr.i), dr.phase, &s.abort, kErrAccumulator);
             if (!ok) break;
             ptx::tc_fence_after();
-            int lowest = blockIdx.x;     // first CTA whose partial sums belong to this tile
+            int lowest = walk.self;     // first CTA (or pair) whose partial sums belong to this tile
             if (!publish && g.k0 > 0) {
                 const int first = g.tile * p.C;
                 while (lowest > 0 && walk.start(lowest) > first) --lowest;
                 // every lane waits for every flag itself: no lane reads a slot it has not acquired
                 const uint64_t t0 = ptx::globaltimer_ns();
-                for (int c = blockIdx.x - 1; ok && c >= lowest; --c) {
+                for (int c = walk.self - 1; ok && c >= lowest; --c) {
                     if (walk.empty(c)) continue;
-                    while (!__all_sync(~0u, (ptx::ld_acquire_gpu(p.flags + c) & kPublishedMask) == 4)) {
+                    while (!__all_sync(~0u, (ptx::ld_acquire_gpu(p.flags + walk.slot(c)) & kPublishedMask) == 4)) {
                         if (__any_sync(~0u, ptx::globaltimer_ns() - t0 > kWaitLimitNs)) {
                             s.abort = 1;
                             atomicOr(&g_tile_error, kErrPartial);
@@ -727,14 +793,14 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             const uint32_t acc = src + dr.i * TN;
             // Other CTAs' sums are added to the accumulator, from the nearest CTA down (a fixed
             // order), with 32 loads in flight per thread: four CTAs' for few tokens, else 32 tokens'.
-            if (lowest < (int)blockIdx.x) {
+            if (lowest < walk.self) {
                 if (g.n <= 8) add_partials<C::kInt8, 4, 8>(p, walk, lowest, row, g.n, acc);
                 else if (TN > 16) add_partials<C::kInt8, 1, 32>(p, walk, lowest, row, g.n, acc);
                 else add_partials<C::kInt8, 4, 8>(p, walk, lowest, row, g.n, acc);
             }
             // Narrow tiles go by eight columns at a time: the loop's code is short (a first pass
             // through it comes from memory) and one token costs one turn.
-            constexpr int kCols = TN <= 64 ? 8 : 32;
+            constexpr int kCols = TN <= 16 ? 8 : TN <= 64 ? 16 : 32;
 #pragma unroll 1
             for (int c0 = 0; c0 < g.n; c0 += kCols) {
                 if (C::kInt8 && !publish && c0 > 0 && c0 % 32 == 0)
@@ -775,15 +841,19 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(sm.d_empty(dr.i));
+            if (lane == 0) {
+                if constexpr (C::kPair) ptx::mbar_arrive_leader(sm.d_empty(dr.i));
+                else ptx::mbar_arrive(sm.d_empty(dr.i));
+            }
             dr.step(C::kDStages);
             if (publish) {
                 if (lane == 0) ptx::atomic_add_release_gpu(p.flags + blockIdx.x, 1);
             } else if (lane == 0) {
                 // The fourth warp to have read a slot frees it for the next call.
-                for (int c = blockIdx.x - 1; c >= lowest; --c) {
+                for (int c = walk.self - 1; c >= lowest; --c) {
                     if (walk.empty(c)) continue;
-                    if (atomicAdd(p.flags + c, kRead) == 4 + 3 * kRead) p.flags[c] = 0;
+                    unsigned* flag = p.flags + walk.slot(c);
+                    if (atomicAdd(flag, kRead) == 4 + 3 * kRead) *flag = 0;
                 }
             }
         }
@@ -797,14 +867,19 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         // A wait gave up: copies and matrix instructions may still be in
         // flight.  Let them end before the memory they use is given up.
         if (warp == 0 && !C::kInt8) drain(r, issued, C::kWStages, sm.w_full(0));
-        if (warp == (C::kInt8 ? 0 : 1)) drain(r, issued, C::kXStages, sm.x_full(0));
+        if (warp == (C::kInt8 ? 0 : 1) && (leader || !C::kInt8)) drain(r, issued, C::kXStages, sm.x_full(0));
         if (warp == 2) {
-            ptx::tc_commit(sm.drained());
+            ptx::tc_commit<C::kPair>(sm.drained());
             ptx::mbar_wait(sm.drained(), 0, kWaitLimitNs);
         }
     }
     if (s.abort) __syncthreads();
-    if (warp == 2) ptx::tmem_free_all(tmem);
+    if constexpr (C::kPair) {
+        // neither CTA's barriers go away while the other may still arrive on them
+        __syncwarp();
+        ptx::cluster_sync();
+    }
+    if (warp == 2) ptx::tmem_free_all<C::kPair>(tmem);
 }
 
 // Packs experts on the device: one thread per 16 bytes of a block's codes (or,
@@ -951,11 +1026,16 @@ int launch(Params p, const void* x, const void* w, int grid, cudaStream_t stream
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kBytes;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    if (C::kPair && grid % 2 != 0) cfg.gridDim.x = --grid;
+    if (grid == 0) return SKINNY_ERR_UNSUPPORTED;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = C::kPair ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, tile_gemm<FMT, TN, SILU>, p, xm, xm2, wm, wm2) == cudaSuccess ? SKINNY_OK : SKINNY_ERR_CUDA;
 }
 

@@ -77,6 +77,8 @@ CASES = [
     ("nvfp4", 260, 1040, [60, 50, 70]),
     ("fp8", 260, 400, [60, 50, 70]),
     ("nvfp4", 2000, 400, [400, 390, 5, 7, 300]),         # whole tiles next to split ones
+    ("nvfp4", 20000, 144, [200, 130, 70, 1, 260]),
+    ("fp8", 10001, 272, [200, 130, 70, 1, 260]),
 ]
 
 

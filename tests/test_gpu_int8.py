@@ -68,7 +68,7 @@ def product(q, rs, c, cs, out):
 @pytest.mark.parametrize("out", [torch.float32, torch.float16])
 @pytest.mark.parametrize("M,N,K", [(1, 128, 128), (1, 1, 16), (3, 129, 48), (8, 5120, 1040), (17, 300, 5120),
                                    (33, 640, 272), (61, 1000, 640), (129, 257, 144), (256, 512, 512),
-                                   (300, 1100, 400), (700, 130, 2064)])
+                                   (300, 1100, 400), (700, 130, 2064), (513, 20000, 272), (100, 30001, 144)])
 def test_product(M, N, K, out, split):
     rng = np.random.default_rng(M + N + K)
     q, c = rng.integers(-128, 128, (M, K), dtype=np.int8), rng.integers(-128, 128, (N, K), dtype=np.int8)
