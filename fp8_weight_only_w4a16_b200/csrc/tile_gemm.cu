@@ -114,7 +114,9 @@ struct Cfg {
     static constexpr int kGroups = kInt8 ? 0 : 2;
     static constexpr int kACol = 512 - 64 * kStepBlocks * kGroups;
     static constexpr int kDecodeWarps = 4 * kGroups;
-    static constexpr int kWarps = 4 + kDecodeWarps + 4;
+    // int8's wide tiles are computed in less time than four warps store them.
+    static constexpr int kEpilogueWarps = kInt8 && kPair ? 8 : 4;
+    static constexpr int kWarps = 4 + kDecodeWarps + kEpilogueWarps;
     static constexpr int kThreads = kWarps * 32;
     static_assert(kInt8 || (kThreads >= kMaxExperts && kWarps <= 32), "make_schedule: a thread per expert");
     // Ring slots.  Experts: weights first, up to what hides HBM's latency (150
@@ -448,12 +450,12 @@ __device__ __forceinline__ void decode(uint32_t src, int row, uint32_t (&v)[2][3
 // Adds the other CTAs' partial sums of a tile (slots of CTAs or pairs self - 1
 // down to `lowest`) to this warp's rows of the accumulator, SLOTS slots and
 // COLS columns at a time.
-template <bool INT8, int SLOTS, int COLS, int TN, bool PAIR>
-__device__ __forceinline__ void add_partials(const Params& p, const Walk<TN, PAIR>& walk, int lowest, int row, int n,
-                                             uint32_t acc)
+template <bool INT8, int SLOTS, int COLS, int TURNS, int TN, bool PAIR>
+__device__ __forceinline__ void add_partials(const Params& p, const Walk<TN, PAIR>& walk, int lowest, int row,
+                                             int turn, int n, uint32_t acc)
 {
 #pragma unroll 1
-    for (int c0 = 0; c0 < n; c0 += COLS) {
+    for (int c0 = turn * COLS; c0 < n; c0 += TURNS * COLS) {
         uint32_t v[COLS];
         ptx::tmem_ld(acc + c0, v);
         const int left = n - c0;
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         for (int i = 0; i < C::kGroups; ++i) ptx::mbar_init(sm.a_full(i), C::kPair ? 8 : 4);
         for (int i = 0; i < C::kDStages; ++i) {
             ptx::mbar_init(sm.d_full(i), 1);
-            ptx::mbar_init(sm.d_empty(i), C::kPair ? 8 : 4);
+            ptx::mbar_init(sm.d_empty(i), C::kEpilogueWarps * (C::kPair ? 2 : 1));
         }
         ptx::mbar_init(sm.drained(), 1);
         ptx::fence_mbar_init();
@@ -708,9 +710,9 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                         if (!ok) break;
                         const uint32_t src = ptx::smem_addr(sm.w(wr.i));
                         const int blocks = C::kStepBlocks == 1 || k + 1 == g.k1 ? 1 : 2;
-                        // one copy of the code for both blocks: the instruction caches hold more of the other roles
-#pragma unroll 1
-                        for (int b = 0; b < blocks; ++b) {
+#pragma unroll
+                        for (int b = 0; b < C::kStepBlocks; ++b) {
+                            if (b >= blocks) break;
                             uint32_t v[2][32];
                             decode<FMT>(src + b * block_bytes(FMT), row, v);
                             if (b == 0 && !first) {
@@ -749,6 +751,9 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         // ---- epilogue: thread = output channel (warp % 4, lane)
         Ring dr;
         const int q = warp & 3, row = q * 32 + lane;
+        // the chunks of columns that this warp stores: one in kTurns
+        constexpr int kTurns = C::kEpilogueWarps / 4;
+        const int turn = (warp - 4 - C::kDecodeWarps) >> 2;
         const uint32_t src = tmem + ((uint32_t)q << 21);
         bool ok = true;
         if (C::kInt8) ptx::pdl_wait_prior_grid();
@@ -765,7 +770,12 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                     scale = p.scale[(size_t)g.e * p.N + o + (SILU && lane >= 16 ? p.outputs : 0)];
                 else scale = p.scale[o];
             }
-            if (C::kInt8 && !publish && lane < g.n) rs = p.row_scale[g.t0 + lane];
+            // Narrow tiles go by few columns at a time: the loop's code is short (a first pass
+            // through it comes from memory) and one token costs one turn.
+            constexpr int kCols = TN <= 16 ? 8 : TN <= 64 ? 16 : 32;
+            constexpr int kNext = kCols * kTurns;
+            const int c_first = turn * kCols;
+            if (C::kInt8 && !publish && c_first + lane < g.n) rs = p.row_scale[g.t0 + c_first + lane];
             ok = wait_warp(sm.d_full(dr.i), dr.phase, &s.abort, kErrAccumulator);
             if (!ok) break;
             ptx::tc_fence_after();
@@ -777,7 +787,8 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                 const uint64_t t0 = ptx::globaltimer_ns();
                 for (int c = walk.self - 1; ok && c >= lowest; --c) {
                     if (walk.empty(c)) continue;
-                    while (!__all_sync(~0u, (ptx::ld_acquire_gpu(p.flags + walk.slot(c)) & kPublishedMask) == 4)) {
+                    while (!__all_sync(~0u, (ptx::ld_acquire_gpu(p.flags + walk.slot(c)) & kPublishedMask) ==
+                                            C::kEpilogueWarps)) {
                         if (__any_sync(~0u, ptx::globaltimer_ns() - t0 > kWaitLimitNs)) {
                             s.abort = 1;
                             atomicOr(&g_tile_error, kErrPartial);
@@ -794,17 +805,14 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             // Other CTAs' sums are added to the accumulator, from the nearest CTA down (a fixed
             // order), with 32 loads in flight per thread: four CTAs' for few tokens, else 32 tokens'.
             if (lowest < walk.self) {
-                if (g.n <= 8) add_partials<C::kInt8, 4, 8>(p, walk, lowest, row, g.n, acc);
-                else if (TN > 16) add_partials<C::kInt8, 1, 32>(p, walk, lowest, row, g.n, acc);
-                else add_partials<C::kInt8, 4, 8>(p, walk, lowest, row, g.n, acc);
+                if (TN > 16 && g.n > 8) add_partials<C::kInt8, 1, 32, kTurns>(p, walk, lowest, row, turn, g.n, acc);
+                else add_partials<C::kInt8, 4, 8, kTurns>(p, walk, lowest, row, turn, g.n, acc);
             }
-            // Narrow tiles go by eight columns at a time: the loop's code is short (a first pass
-            // through it comes from memory) and one token costs one turn.
-            constexpr int kCols = TN <= 16 ? 8 : TN <= 64 ? 16 : 32;
 #pragma unroll 1
-            for (int c0 = 0; c0 < g.n; c0 += kCols) {
-                if (C::kInt8 && !publish && c0 > 0 && c0 % 32 == 0)
-                    rs = c0 + lane < g.n ? p.row_scale[g.t0 + c0 + lane] : 0.f;
+            for (int c0 = c_first; c0 < g.n; c0 += kNext) {
+                // the next chunk's row scales, ahead of this one's stores
+                float rs_next = 0.f;
+                if (C::kInt8 && !publish && c0 + kNext + lane < g.n) rs_next = p.row_scale[g.t0 + c0 + kNext + lane];
                 uint32_t v[kCols];
                 ptx::tmem_ld(acc + c0, v);
                 const int left = g.n - c0;
@@ -833,11 +841,12 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                     float r[kCols];
 #pragma unroll
                     for (int j = 0; j < kCols; ++j) {
-                        if constexpr (C::kInt8) r[j] = (float)(int)v[j] * __shfl_sync(~0u, rs, c0 % 32 + j) * scale;
+                        if constexpr (C::kInt8) r[j] = (float)(int)v[j] * __shfl_sync(~0u, rs, j) * scale;
                         else r[j] = __uint_as_float(v[j]) * scale;
                     }
                     put_column<kCols>(p.y, at, p.outputs, r, valid ? left : 0, p.out_f32);
                 }
+                rs = rs_next;
             }
             ptx::tc_fence_before();
             __syncwarp();
@@ -849,11 +858,11 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             if (publish) {
                 if (lane == 0) ptx::atomic_add_release_gpu(p.flags + blockIdx.x, 1);
             } else if (lane == 0) {
-                // The fourth warp to have read a slot frees it for the next call.
+                // The last warp to have read a slot frees it for the next call.
                 for (int c = walk.self - 1; c >= lowest; --c) {
                     if (walk.empty(c)) continue;
                     unsigned* flag = p.flags + walk.slot(c);
-                    if (atomicAdd(flag, kRead) == 4 + 3 * kRead) *flag = 0;
+                    if (atomicAdd(flag, kRead) == C::kEpilogueWarps + (C::kEpilogueWarps - 1) * kRead) *flag = 0;
                 }
             }
         }
