@@ -462,7 +462,7 @@ typedef enum { SKINNY_PROB_F16 = 0, SKINNY_PROB_F32 = 1, SKINNY_PROB_BF16 = 2 } 
  *                 [0, S] count as the nearest), or NULL for S each.
  *   tokens        device int32 [B][S+1]: the accepted drafts, the drawn token, then -1.
  *   accepted      device int32 [B]: how many drafts were accepted.
- * Weights that are not finite count as 0.  Where max(p - q, 0) has no positive
+ * Weights that are not finite in FP32 count as 0.  Where max(p - q, 0) has no positive
  * weight, the draw is from p; where p has none either, the token is -1.
  * S = 0 draws one token from each target row.
  * Errors: INVALID_ARG, ALIGNMENT; UNSUPPORTED for B > 2^20, S > 1024 or V > 2^28. */
