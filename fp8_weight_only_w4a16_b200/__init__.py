@@ -467,22 +467,14 @@ def _launch(name, d, stream, *args) -> None:
     """Calls the library's `name` with the stream as its last argument, with device d current."""
     import torch
 
-    fn = getattr(library(), name)
-    if d == torch.cuda.current_device():
-        st = fn(*args, _raw_stream(d) if stream is None else stream.cuda_stream)
+    fn = getattr(_lib or library(), name)
+    if d == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(d):
-            st = fn(*args, _raw_stream(d) if stream is None else stream.cuda_stream)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream)
     if st != OK:
         raise SkinnyError(st, name)
-
-
-def _raw_stream(d: int) -> int:
-    """Handle of the current stream of device d."""
-    import torch
-
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # without building a Stream object
-    return raw(d) if raw is not None else torch.cuda.current_stream(d).cuda_stream
 
 
 def _ws(workspace):
@@ -494,12 +486,11 @@ def _ws(workspace):
 def _out_code(y, rows, cols):
     import torch
 
-    if y.dim() != 2 or y.shape[0] != rows or y.shape[1] != cols or not y.is_contiguous():
-        raise ValueError("y must be a contiguous float16/float32 [%d, %d] tensor" % (rows, cols))
-    if y.dtype == torch.float16:
-        return OUT_F16
-    if y.dtype == torch.float32:
-        return OUT_F32
+    if y.shape == (rows, cols) and y.is_contiguous():
+        if y.dtype == torch.float16:
+            return OUT_F16
+        if y.dtype == torch.float32:
+            return OUT_F32
     raise ValueError("y must be a contiguous float16/float32 [%d, %d] tensor" % (rows, cols))
 
 
@@ -640,7 +631,7 @@ def gemm_experts(x, w, offsets, out_dtype=None, workspace=None, stream=None):
     gemm_experts_into.  Rows of no expert are not written."""
     import torch
 
-    y = torch.empty((x.shape[0], w.N), dtype=out_dtype or torch.float16, device=x.device)
+    y = x.new_empty((x.shape[0], w.N), dtype=out_dtype or torch.float16)
     gemm_experts_into(y, x, w, offsets, workspace=workspace, stream=stream)
     return y
 
@@ -655,7 +646,7 @@ def gemm_experts_silu_mul(x, w, offsets, out_dtype=None, workspace=None, stream=
     """Allocate y [T, N/2]: see gemm_experts_silu_mul_into."""
     import torch
 
-    y = torch.empty((x.shape[0], w.N // 2), dtype=out_dtype or torch.float16, device=x.device)
+    y = x.new_empty((x.shape[0], w.N // 2), dtype=out_dtype or torch.float16)
     gemm_experts_silu_mul_into(y, x, w, offsets, workspace=workspace, stream=stream)
     return y
 
@@ -704,8 +695,8 @@ def quantize_int8(x, stream=None):
     """Allocate and return (q int8 [M, K], row_scale float32 [M]): see quantize_int8_into."""
     import torch
 
-    q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-    row_scale = torch.empty(x.shape[:1], dtype=torch.float32, device=x.device)
+    q = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
+    row_scale = x.new_empty(x.shape[0], dtype=torch.float32)
     quantize_int8_into(q, row_scale, x, stream=stream)
     return q, row_scale
 
@@ -715,15 +706,16 @@ def gemm_int8_into(y, q, row_scale, w: "WeightInt8", workspace=None, stream=None
     (y float16 or float32, preallocated; any number of rows)."""
     import torch
 
-    if q.dim() != 2 or q.dtype != torch.int8 or not q.is_contiguous() or q.shape[1] != w.K:
-        raise ValueError("q must be a contiguous int8 [M, %d] tensor" % w.K)
+    N, K = w.codes.shape
+    if q.dtype != torch.int8 or q.dim() != 2 or q.shape[1] != K or not q.is_contiguous():
+        raise ValueError("q must be a contiguous int8 [M, %d] tensor" % K)
     M = q.shape[0]
-    if row_scale.dtype != torch.float32 or row_scale.dim() != 1 or row_scale.shape[0] != M or not row_scale.is_contiguous():
+    if row_scale.dtype != torch.float32 or row_scale.shape != (M,) or not row_scale.is_contiguous():
         raise ValueError("row_scale must be a contiguous float32 [M] tensor")
-    out = _out_code(y, M, w.N)
+    out = _out_code(y, M, N)
     ws_ptr, ws_bytes = _ws(workspace)
     _launch("skinny_int8_gemm", _device_of(q, y, row_scale, w.codes, w.channel_scale, workspace), stream, q.data_ptr(),
-            row_scale.data_ptr(), M, w.K, w.codes.data_ptr(), w.channel_scale.data_ptr(), w.N, y.data_ptr(), out, ws_ptr,
+            row_scale.data_ptr(), M, K, w.codes.data_ptr(), w.channel_scale.data_ptr(), N, y.data_ptr(), out, ws_ptr,
             ws_bytes)
 
 
@@ -731,7 +723,7 @@ def gemm_int8(q, row_scale, w: "WeightInt8", out_dtype=None, workspace=None, str
     """Allocate y [M, N] (float16 unless out_dtype says otherwise): see gemm_int8_into."""
     import torch
 
-    y = torch.empty((q.shape[0], w.N), dtype=out_dtype or torch.float16, device=q.device)
+    y = q.new_empty((q.shape[0], w.codes.shape[0]), dtype=out_dtype or torch.float16)
     gemm_int8_into(y, q, row_scale, w, workspace=workspace, stream=stream)
     return y
 
@@ -770,28 +762,36 @@ def verify_draft_into(tokens, accepted, target, draft, draft_tokens, uniform, nu
     import torch
 
     kind = _prob_dtypes().get(target.dtype)
-    if kind is None or target.dim() != 3 or target.shape[1] < 1 or target.shape[2] < 1:
+    if kind is None or target.dim() != 3:
         raise ValueError("target must be a float32/float16/bfloat16 [B, S+1, V] tensor")
-    B, S, V = target.shape[0], target.shape[1] - 1, target.shape[2]
-    if V > 1 and target.stride(2) != 1:
+    B, S, V = target.shape
+    S -= 1
+    if S < 0 or V < 1:
+        raise ValueError("target must be a float32/float16/bfloat16 [B, S+1, V] tensor")
+    target_b, target_s, one = target.stride()
+    if V > 1 and one != 1:
         raise ValueError("target must have unit stride along V")
+    draft_ptr, draft_b, draft_s = None, 0, 0
     if draft is not None:
-        if tuple(draft.shape) != (B, S, V) or draft.dtype != target.dtype:
+        if draft.dtype != target.dtype or draft.shape != (B, S, V):
             raise ValueError("draft must be a [%d, %d, %d] tensor of target's dtype" % (B, S, V))
-        if V > 1 and draft.stride(2) != 1:
+        draft_b, draft_s, one = draft.stride()
+        if V > 1 and one != 1:
             raise ValueError("draft must have unit stride along V")
-    for t, shape, dtype, what in ((draft_tokens, (B, S), torch.int32, "draft_tokens"),
-                                  (uniform, (B, S + 1), torch.float32, "uniform"),
-                                  (num_drafts, (B,), torch.int32, "num_drafts"),
-                                  (tokens, (B, S + 1), torch.int32, "tokens"), (accepted, (B,), torch.int32, "accepted")):
-        if t is None and what == "num_drafts":
-            continue
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous %s %s tensor" % (what, dtype, list(shape)))
+        draft_ptr = draft.data_ptr() if S > 0 else None
+    i32, shape = torch.int32, (B, S + 1)
+    if draft_tokens.dtype != i32 or draft_tokens.shape != (B, S) or not draft_tokens.is_contiguous():
+        raise ValueError("draft_tokens must be a contiguous int32 [%d, %d] tensor" % (B, S))
+    if uniform.dtype != torch.float32 or uniform.shape != shape or not uniform.is_contiguous():
+        raise ValueError("uniform must be a contiguous float32 [%d, %d] tensor" % shape)
+    if num_drafts is not None and (num_drafts.dtype != i32 or num_drafts.shape != (B,) or not num_drafts.is_contiguous()):
+        raise ValueError("num_drafts must be a contiguous int32 [%d] tensor" % B)
+    if tokens.dtype != i32 or tokens.shape != shape or not tokens.is_contiguous():
+        raise ValueError("tokens must be a contiguous int32 [%d, %d] tensor" % shape)
+    if accepted.dtype != i32 or accepted.shape != (B,) or not accepted.is_contiguous():
+        raise ValueError("accepted must be a contiguous int32 [%d] tensor" % B)
     d = _device_of(target, draft, draft_tokens, uniform, num_drafts, tokens, accepted)
-    has = draft is not None and S > 0
-    _launch("skinny_verify_draft", d, stream, target.data_ptr(), target.stride(0), target.stride(1),
-            draft.data_ptr() if has else None, draft.stride(0) if has else 0, draft.stride(1) if has else 0, kind,
+    _launch("skinny_verify_draft", d, stream, target.data_ptr(), target_b, target_s, draft_ptr, draft_b, draft_s, kind,
             draft_tokens.data_ptr() if S else None, uniform.data_ptr(),
             num_drafts.data_ptr() if num_drafts is not None else None, B, S, V, tokens.data_ptr(), accepted.data_ptr())
 
@@ -800,7 +800,7 @@ def verify_draft(target, draft, draft_tokens, uniform, num_drafts=None, stream=N
     """Allocate and return (tokens int32 [B, S+1], accepted int32 [B]): see verify_draft_into."""
     import torch
 
-    tokens = torch.empty(target.shape[:2], dtype=torch.int32, device=target.device)
-    accepted = torch.empty(target.shape[:1], dtype=torch.int32, device=target.device)
+    tokens = torch.empty_like(uniform, dtype=torch.int32, memory_format=torch.contiguous_format)
+    accepted = uniform.new_empty(uniform.shape[0], dtype=torch.int32)
     verify_draft_into(tokens, accepted, target, draft, draft_tokens, uniform, num_drafts, stream=stream)
     return tokens, accepted
