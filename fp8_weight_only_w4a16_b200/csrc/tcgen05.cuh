@@ -213,9 +213,9 @@ __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map)
 }
 
 // A flag that one CTA publishes for another.
-__device__ __forceinline__ void atomic_add_release_gpu(unsigned* p, unsigned v)
+__device__ __forceinline__ void st_release_gpu(unsigned* p, unsigned v)
 {
-    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 __device__ __forceinline__ unsigned ld_acquire_gpu(const unsigned* p)
 {

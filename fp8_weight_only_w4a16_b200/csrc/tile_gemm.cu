@@ -53,10 +53,10 @@ constexpr unsigned kErrPartial = 4u;      // another CTA's partial sums
 
 __device__ unsigned int g_tile_error;
 
-// A slot's flag in the workspace: its low byte counts the epilogue warps that
-// have published their rows, the rest (in units of kRead) those that have read
-// them.  Zero between calls.
-constexpr unsigned kPublishedMask = 0xFF, kRead = 0x100;
+// A slot's flags in the workspace: one for each epilogue warp, set when that
+// warp has published its rows and columns, and cleared by the one warp that
+// reads them (the same warp of another CTA).  Zero between calls.
+constexpr int kFlags = 8;
 
 // Bytes of one packed 128 x 128 block.  A decoder thread reads its row's 128
 // columns as 16-byte words, 128 rows side by side (no bank conflicts):
@@ -71,10 +71,11 @@ struct Params {
     const float* row_scale;      // int8 [T]
     const int32_t* offsets;      // experts [E + 1]
     void* y;                     // [T][outputs]
-    unsigned* partials;          // workspace: [P][kSlotWords], then [P] flags (or null)
+    unsigned* partials;          // workspace: [P][kSlotWords], then [P][kFlags] flags (or null)
     unsigned* flags;
     int T, N, K, E;
     int G, C;                    // row tiles, K blocks
+    float rcp_C, rcp_groups;     // 1 / C, 1 / (row tiles, or pairs of them)
     int outputs;                 // outputs per token: N, or N / 2 (SiLU*mul)
     int out_f32;
 };
@@ -118,7 +119,6 @@ struct Cfg {
     static constexpr int kEpilogueWarps = kInt8 && kPair ? 8 : 4;
     static constexpr int kWarps = 4 + kDecodeWarps + kEpilogueWarps;
     static constexpr int kThreads = kWarps * 32;
-    static_assert(kInt8 || (kThreads >= kMaxExperts && kWarps <= 32), "make_schedule: a thread per expert");
     // Ring slots.  Experts: weights first, up to what hides HBM's latency (150
     // KB; a wide tile asks for less), and the tokens' ring takes the rest.
     // int8 slots hold weights and tokens.
@@ -145,9 +145,8 @@ struct Cfg {
 struct Schedule {
     int tiles[kMaxExperts + 1];          // running number of tiles
     int rows[kMaxExperts + 1];           // running row offset (offsets made monotone and clamped to [0, T])
-    uint32_t warp_tot_tiles[32];         // one entry per warp of the block
-    int warp_max[32];
     int total;
+    int splits, share, extra;            // see Walk
     uint32_t tmem;
     int abort;
 };
@@ -174,11 +173,37 @@ __device__ __forceinline__ int find(const int* a, int n, int v)
     return lo;
 }
 
+// Which tiles are split, and how their blocks are shared out (see Walk).
+template <bool PAIR>
+__device__ __forceinline__ void finish_schedule(Schedule& s, const Params& p, int total)
+{
+    const int P = PAIR ? gridDim.x / 2 : gridDim.x;
+    int splits = 0;
+    if (p.partials != nullptr) {
+        const int rest = total % P;
+        splits = rest == 0 || 4 * rest >= P || total < P ? rest : rest + P;
+    }
+    s.total = total;
+    s.splits = splits;
+    s.share = splits * p.C / P;
+    s.extra = splits * p.C % P;
+}
+
 // A piece of one CTA's work: K blocks [k0, k1) of a tile.
 struct Segment {
     int e, row_tile, t0, n;   // expert, this CTA's row tile, first token row, token rows
     int tile, k0, k1;
 };
+
+// x / d for 0 <= x < 2^31 where the quotient is below 2^22; rcp = 1.f / d.
+__device__ __forceinline__ int quotient(int x, int d, float rcp)
+{
+    int q = (int)((float)x * rcp);
+    const int r = x - q * d;
+    q += r >= d;
+    q -= r < 0;
+    return q;
+}
 
 // The CTA's pieces.  Whole tiles are dealt out one after another, so that the
 // CTAs work on neighbouring tiles and share their operands in L2.  What would
@@ -195,34 +220,26 @@ struct Walk {
     const Schedule& s;
     const Params& p;
     int P, self;        // CTAs (or pairs) of the grid, and which this is
-    int share, extra;   // split blocks: CTA b has share + (b < extra)
-    int u0, u;          // this CTA's first block, and one past the next piece's last
+    int u0, u;          // this CTA's first split block, and one past the next piece's last
     int tile;           // the next whole tile
 
     __device__ Walk(const Schedule& s_, const Params& p_) : s(s_), p(p_)
     {
         P = PAIR ? gridDim.x / 2 : gridDim.x;
         self = PAIR ? blockIdx.x / 2 : blockIdx.x;
-        const int b = self;
-        int splits = 0;
-        if (p.partials != nullptr) {
-            const int rest = s.total % P;
-            splits = rest == 0 || 4 * rest >= P ? rest : s.total < P ? rest : rest + P;
-        }
-        share = splits * p.C / P;
-        extra = splits * p.C % P;
-        u0 = start(b);
-        u = start(b + 1);
-        tile = splits + b;
+        u0 = start(self);
+        u = start(self + 1);
+        tile = s.splits + self;
     }
-    __device__ int start(int b) const { return b * share + (b < extra ? b : extra); }
+    // split blocks: CTA b has share + (b < extra)
+    __device__ int start(int b) const { return b * s.share + (b < s.extra ? b : s.extra); }
     // the workspace slot that this CTA reads of CTA (or pair) b
     __device__ int slot(int b) const { return PAIR ? 2 * b + (int)(blockIdx.x & 1) : b; }
-    __device__ bool empty(int b) const { return share == 0 && b >= extra; }
+    __device__ bool empty(int b) const { return s.share == 0 && b >= s.extra; }
     __device__ bool next(Segment& g)
     {
         if (u > u0) {
-            g.tile = (u - 1) / p.C;
+            g.tile = quotient(u - 1, p.C, p.rcp_C);
             g.k1 = u - g.tile * p.C;
             g.k0 = u0 > g.tile * p.C ? u0 - g.tile * p.C : 0;
             u = g.tile * p.C + g.k0;
@@ -235,11 +252,11 @@ struct Walk {
         }
         g.e = find(s.tiles, p.E, g.tile);
         const int m = s.rows[g.e + 1] - s.rows[g.e];
-        const int q = tile_rows(m, token_tiles(m, TN));
+        const int q = m <= TN ? (m + 15) & ~15 : tile_rows(m, token_tiles(m, TN));
         const int lt = g.tile - s.tiles[g.e];
-        const int groups = row_groups<PAIR>(p);
-        g.row_tile = PAIR ? lt % groups * 2 + (int)(blockIdx.x & 1) : lt % groups;
-        const int t = lt / groups * q;
+        const int groups = row_groups<PAIR>(p), tt = quotient(lt, groups, p.rcp_groups), rt = lt - tt * groups;
+        g.row_tile = PAIR ? rt * 2 + (int)(blockIdx.x & 1) : rt;
+        const int t = tt * q;
         g.t0 = s.rows[g.e] + t;
         g.n = m - t < q ? m - t : q;
         return true;
@@ -364,32 +381,41 @@ __device__ __forceinline__ uint32_t warp_scan_add(uint32_t v)
     return v;
 }
 
-// The experts' schedule, by the whole block (a thread per expert).
+// The experts' schedule, by one warp: a lane takes neighbouring experts.
 // Offsets are device data that the host has not seen: they are clamped to
 // [0, T] and made non-decreasing, so no row is outside x and y or has two experts.
 template <int TN, bool PAIR>
 __device__ void make_schedule(Schedule& s, const Params& p)
 {
-    const int i = threadIdx.x, w = i / 32;
+    const int lane = threadIdx.x & 31, per = (p.E + 31) / 32;
+    const int e0 = lane * per < p.E ? lane * per : p.E, e1 = e0 + per < p.E ? e0 + per : p.E;
     auto clamp = [&](int v) { return v < 0 ? 0 : v > p.T ? p.T : v; };
     const int first = clamp(p.offsets[0]);
-    int v = i < p.E ? clamp(p.offsets[i + 1]) : 0;
-    v = v > first ? v : first;
-    v = warp_scan_max(v);
-    if ((i & 31) == 31) s.warp_max[w] = v;
-    __syncthreads();
-    for (int k = 0; k < w; ++k) v = v > s.warp_max[k] ? v : s.warp_max[k];
-    if (i == 0) s.rows[0] = first;
-    if (i < p.E) s.rows[i + 1] = v;
-    __syncthreads();
-    uint32_t n = i < p.E ? (uint32_t)token_tiles(s.rows[i + 1] - s.rows[i], TN) * (uint32_t)row_groups<PAIR>(p) : 0;
-    n = warp_scan_add(n);
-    if ((i & 31) == 31) s.warp_tot_tiles[w] = n;
-    __syncthreads();
-    for (int k = 0; k < w; ++k) n += s.warp_tot_tiles[k];
-    if (i == 0) s.tiles[0] = 0;
-    if (i < p.E) s.tiles[i + 1] = (int)n;
-    if (i == p.E - 1) s.total = (int)n;
+    int top = first;
+    for (int e = e0; e < e1; ++e) {
+        const int v = clamp(p.offsets[e + 1]);
+        top = top > v ? top : v;
+        s.rows[e + 1] = top;
+    }
+    int before = __shfl_up_sync(~0u, warp_scan_max(top), 1);
+    before = lane == 0 ? first : before;
+    const int groups = row_groups<PAIR>(p);
+    int prev = before, n = 0;
+    for (int e = e0; e < e1; ++e) {
+        const int v = s.rows[e + 1] > before ? s.rows[e + 1] : before;
+        s.rows[e + 1] = v;
+        n += token_tiles(v - prev, TN) * groups;
+        s.tiles[e + 1] = n;
+        prev = v;
+    }
+    const int run = (int)warp_scan_add((uint32_t)n);
+    for (int e = e0; e < e1; ++e) s.tiles[e + 1] += run - n;
+    if (lane == 0) {
+        s.rows[0] = first;
+        s.tiles[0] = 0;
+    }
+    if (lane == 31) finish_schedule<PAIR>(s, p, run);
+    __syncwarp();
 }
 
 // Stores r[0..n) at y[at], y[at + step], ...
@@ -481,6 +507,76 @@ __device__ __forceinline__ void add_partials(const Params& p, const Walk<TN, PAI
     ptx::tmem_wait_st();
 }
 
+// The W producer's thread: weight slots in the order of the walk.
+template <int FMT, int TN>
+struct Producer {
+    using C = Cfg<FMT, TN>;
+    int u0, u, tile;      // the walk's position
+    int k, k1;            // blocks of the current piece
+    int rt;               // its row tile
+    uint32_t pair_bytes;  // int8 pairs: what both CTAs' copies of a step bring
+    const uint8_t* src;
+    bool ok;
+
+    __device__ __forceinline__ void begin(const Schedule& s, const Params& p)
+    {
+        const Walk<TN, C::kPair> w(s, p);
+        u0 = w.u0, u = w.u, tile = w.tile;
+        k = k1 = 0;
+        ok = true;
+    }
+    // Fills slots until `most` have been issued or the walk ends.
+    __device__ __forceinline__ void produce(const Shared<FMT, TN>& sm, Ring& r, int& issued, int most, Schedule& s,
+                                            const Params& p, const CUtensorMap* w_map, const CUtensorMap* w_map2,
+                                            bool leader)
+    {
+        const uint64_t pol = TN <= 32 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
+        while (ok && issued < most) {
+            if (k >= k1) {
+                Walk<TN, C::kPair> w(s, p);
+                w.u = u, w.tile = tile;
+                Segment g;
+                if (!w.next(g)) {
+                    ok = false;
+                    return;
+                }
+                u = w.u, tile = w.tile;
+                k = g.k0, k1 = g.k1;
+                // (an odd last row tile has no partner: its pair's second CTA computes it too, and stores nothing)
+                rt = C::kPair && g.row_tile >= p.G ? p.G - 1 : g.row_tile;
+                src = C::kInt8 ? nullptr : p.w + ((size_t)g.e * p.G + rt) * p.C * block_bytes(FMT);
+                pair_bytes = 2 * (C::kWBytes + (((g.n + 15) & ~15) / 2 + C::kBox - 1) / C::kBox * C::kBox * 128);
+            }
+            ok = wait(C::kInt8 ? sm.x_empty(r.i) : sm.w_empty(r.i), r.phase ^ 1, &s.abort, kErrRing);
+            if (!ok) return;
+            if constexpr (C::kInt8 && C::kPair) {
+                // the leader's barrier counts both CTAs' weights and tokens
+                uint64_t* full = sm.x_full(r.i);
+                if (leader) ptx::mbar_arrive_expect_tx(full, pair_bytes);
+                ptx::tma_load_2d_pair(sm.w(r.i), w_map, k * kBlockK, rt * kRows, ptx::leader_addr(full), pol);
+            } else if constexpr (C::kInt8) {
+                uint64_t* full = sm.x_full(r.i);
+                ptx::mbar_arrive_expect_tx(full, C::kWBytes);
+                if (C::kW3d && (k + 2) * kBlockK <= p.K) {
+                    ptx::tma_load_3d(sm.w(r.i), w_map, 0, rt * kRows, k, full, pol);
+                } else {
+                    // plain boxes: past K they fill in zeros
+                    for (int b = 0; b < C::kStepBlocks; ++b)
+                        ptx::tma_load_2d(sm.w(r.i) + b * block_bytes(FMT), C::kW3d ? w_map2 : w_map, (k + b) * kBlockK,
+                                         rt * kRows, full, pol);
+                }
+            } else {
+                const uint32_t bytes = (C::kStepBlocks == 2 && k + 1 < k1 ? 2 : 1) * block_bytes(FMT);
+                ptx::mbar_arrive_expect_tx(sm.w_full(r.i), bytes);
+                ptx::bulk_g2s(sm.w(r.i), src + (size_t)k * block_bytes(FMT), bytes, sm.w_full(r.i), pol);
+            }
+            r.step(C::kWStages);
+            ++issued;
+            k += C::kStepBlocks;
+        }
+    }
+};
+
 template <int FMT, int TN, bool SILU>
 __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
     tile_gemm(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap x_map,
@@ -515,6 +611,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         s.abort = 0;
     }
     if (warp == 2) ptx::tmem_alloc_all<C::kPair>(&s.tmem);
+    __syncwarp();
     const int rank = C::kPair ? (int)ptx::cluster_rank() : 0;
     const bool leader = rank == 0;
     ptx::pdl_launch_dependents();
@@ -525,12 +622,26 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             s.rows[0] = 0;
             s.rows[1] = p.T;
             s.tiles[0] = 0;
-            s.tiles[1] = s.total = token_tiles(p.T, TN) * row_groups<C::kPair>(p);
+            s.tiles[1] = token_tiles(p.T, TN) * row_groups<C::kPair>(p);
+            finish_schedule<C::kPair>(s, p, s.tiles[1]);
         }
     } else {
         ptx::pdl_wait_prior_grid();
-        make_schedule<TN, C::kPair>(s, p);
+        if (warp == 0) make_schedule<TN, C::kPair>(s, p);
     }
+    Ring r;            // position of a single-thread role, and how much it has issued
+    int issued = 0;
+    // The single-thread roles run under elect.sync, which tells the compiler
+    // that one thread is active: a matrix instruction of 16 columns then issues
+    // every 9 clocks, under `lane == 0` every 68 (measured on B200).
+    bool mine = false;
+    Producer<FMT, TN> producer;
+    if (!C::kInt8 && warp == 0 && ptx::elect_one()) {
+        // the warp that made the schedule fills its ring before the CTA is ready
+        producer.begin(s, p);
+        producer.produce(sm, r, issued, C::kWStages, s, p, &w_map, &w_map2, leader);
+    }
+    __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
     if constexpr (C::kPair) ptx::cluster_sync();      // the other CTA's barriers are ready, too
@@ -538,57 +649,13 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
     const uint32_t tmem = s.tmem;
     Walk<TN, C::kPair> walk(s, p);
     Segment g;
-    Ring r;            // position of a single-thread role, and how much it has issued
-    int issued = 0;
-    // The single-thread roles run under elect.sync, which tells the compiler
-    // that one thread is active: a matrix instruction of 16 columns then issues
-    // every 9 clocks, under `lane == 0` every 68 (measured on B200).
-    bool mine = false;
 
     if (warp == 0) {
         // ---- W producer
         if (ptx::elect_one()) {
             mine = true;
-            bool ok = true;
-            const uint64_t pol = TN <= 32 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
-            while (ok && walk.next(g)) {
-                // (an odd last row tile has no partner: its pair's second CTA computes it too, and stores nothing)
-                const int rt = C::kPair && g.row_tile >= p.G ? p.G - 1 : g.row_tile;
-                const uint8_t* src = C::kInt8 ? nullptr : p.w + ((size_t)g.e * p.G + rt) * p.C * block_bytes(FMT);
-                const uint32_t pair_bytes =
-                    2 * (C::kWBytes + (((g.n + 15) & ~15) / 2 + C::kBox - 1) / C::kBox * C::kBox * 128);
-                for (int k = g.k0; k < g.k1; k += C::kStepBlocks) {
-                    ok = wait(C::kInt8 ? sm.x_empty(r.i) : sm.w_empty(r.i), r.phase ^ 1, &s.abort, kErrRing);
-                    if (!ok) break;
-                    if constexpr (C::kInt8) {
-                        uint64_t* full = sm.x_full(r.i);
-                        if constexpr (C::kPair) {
-                            // the leader's barrier counts both CTAs' weights and tokens
-                            if (leader) ptx::mbar_arrive_expect_tx(full, pair_bytes);
-                            ptx::tma_load_2d_pair(sm.w(r.i), &w_map, k * kBlockK, rt * kRows, ptx::leader_addr(full),
-                                                  pol);
-                            r.step(C::kWStages);
-                            ++issued;
-                            continue;
-                        }
-                        ptx::mbar_arrive_expect_tx(full, C::kWBytes);
-                        if (C::kW3d && (k + 2) * kBlockK <= p.K) {
-                            ptx::tma_load_3d(sm.w(r.i), &w_map, 0, g.row_tile * kRows, k, full, pol);
-                        } else {
-                            // plain boxes: past K they fill in zeros
-                            for (int b = 0; b < C::kStepBlocks; ++b)
-                                ptx::tma_load_2d(sm.w(r.i) + b * block_bytes(FMT), C::kW3d ? &w_map2 : &w_map,
-                                                 (k + b) * kBlockK, g.row_tile * kRows, full, pol);
-                        }
-                    } else {
-                        const uint32_t bytes = (C::kStepBlocks == 2 && k + 1 < g.k1 ? 2 : 1) * block_bytes(FMT);
-                        ptx::mbar_arrive_expect_tx(sm.w_full(r.i), bytes);
-                        ptx::bulk_g2s(sm.w(r.i), src + (size_t)k * block_bytes(FMT), bytes, sm.w_full(r.i), pol);
-                    }
-                    r.step(C::kWStages);
-                    ++issued;
-                }
-            }
+            if (C::kInt8) producer.begin(s, p);
+            producer.produce(sm, r, issued, 0x7FFFFFFF, s, p, &w_map, &w_map2, leader);
         }
     } else if (warp == 1) {
         // ---- x producer
@@ -783,12 +850,13 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             if (!publish && g.k0 > 0) {
                 const int first = g.tile * p.C;
                 while (lowest > 0 && walk.start(lowest) > first) --lowest;
-                // every lane waits for every flag itself: no lane reads a slot it has not acquired
+                // lane i waits for the i-th CTA below, 32 at a time
                 const uint64_t t0 = ptx::globaltimer_ns();
-                for (int c = walk.self - 1; ok && c >= lowest; --c) {
-                    if (walk.empty(c)) continue;
-                    while (!__all_sync(~0u, (ptx::ld_acquire_gpu(p.flags + walk.slot(c)) & kPublishedMask) ==
-                                            C::kEpilogueWarps)) {
+                for (int c = walk.self - 1; ok && c >= lowest; c -= 32) {
+                    const int other = c - lane;
+                    const bool there = other >= lowest && !walk.empty(other);
+                    const unsigned* flag = p.flags + walk.slot(there ? other : c) * kFlags + turn * 4 + q;
+                    while (!__all_sync(~0u, !there || ptx::ld_acquire_gpu(flag) != 0)) {
                         if (__any_sync(~0u, ptx::globaltimer_ns() - t0 > kWaitLimitNs)) {
                             s.abort = 1;
                             atomicOr(&g_tile_error, kErrPartial);
@@ -799,6 +867,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                         }
                     }
                 }
+                __syncwarp();      // the other lanes' loads follow what each lane has acquired
                 if (!ok) break;
             }
             const uint32_t acc = src + dr.i * TN;
@@ -856,14 +925,9 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             }
             dr.step(C::kDStages);
             if (publish) {
-                if (lane == 0) ptx::atomic_add_release_gpu(p.flags + blockIdx.x, 1);
-            } else if (lane == 0) {
-                // The last warp to have read a slot frees it for the next call.
-                for (int c = walk.self - 1; c >= lowest; --c) {
-                    if (walk.empty(c)) continue;
-                    unsigned* flag = p.flags + walk.slot(c);
-                    if (atomicAdd(flag, kRead) == C::kEpilogueWarps + (C::kEpilogueWarps - 1) * kRead) *flag = 0;
-                }
+                if (lane == 0) ptx::st_release_gpu(p.flags + blockIdx.x * kFlags + turn * 4 + q, 1);
+            } else {
+                for (int c = walk.self - 1 - lane; c >= lowest; c -= 32) p.flags[walk.slot(c) * kFlags + turn * 4 + q] = 0;
             }
         }
     }
@@ -1016,12 +1080,14 @@ bool make_map(CUtensorMap* map, const void* base, bool f16, int64_t rows, int64_
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t workspace_size(int sms) { return (size_t)sms * (kSlotWords + 1) * 4; }
+size_t workspace_size(int sms) { return (size_t)sms * (kSlotWords + kFlags) * 4; }
 
 template <int FMT, int TN, bool SILU>
 int launch(Params p, const void* x, const void* w, int grid, cudaStream_t stream)
 {
     using C = Cfg<FMT, TN>;
+    p.rcp_C = 1.f / p.C;
+    p.rcp_groups = 1.f / (C::kPair ? (p.G + 1) / 2 : p.G);
     CUtensorMap xm, xm2, wm, wm2;
     if (!make_map(&xm, x, !C::kInt8, p.T, p.K, C::kBox, C::kX3d ? C::kChunks : 1)) return SKINNY_ERR_CUDA;
     wm = wm2 = xm2 = xm;

@@ -355,7 +355,7 @@ int skinny_debug_static_workspace_address(void** addr);
 #define SKINNY_MAX_INT8_K 131056
 
 /* Size of the workspace of the calls below on the current device (128 KB and
- * one flag per SM).  SKINNY_OK, or INVALID_ARG (null bytes) / CUDA. */
+ * 32 bytes of flags per SM).  SKINNY_OK, or INVALID_ARG (null bytes) / CUDA. */
 int skinny_tile_workspace_bytes(size_t* bytes);
 
 /* Bytes of E packed experts of N x K weights each, in format fmt (a

@@ -94,7 +94,7 @@ def test_store(fmt, N, K, counts, out, split):
     ref, bound = expected(fmt, logical, x, off)
     assert_parity(y.double().cpu().numpy(), ref, bound, out, "%s %dx%d %s" % (fmt, N, K, counts))
     if ws is not None:    # the flags are free again
-        assert not ws[-4 * torch.cuda.get_device_properties(0).multi_processor_count:].any()
+        assert not ws[-32 * torch.cuda.get_device_properties(0).multi_processor_count:].any()
 
 
 @pytest.mark.parametrize("out", ["f32", "f16"])
