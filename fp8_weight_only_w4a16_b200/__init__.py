@@ -483,14 +483,18 @@ def _ws(workspace):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _out_code(y, rows, cols):
+def _output(y, x, rows, cols, out_dtype):
+    """(y, its SKINNY_OUT code); y None: a new tensor on x's device."""
     import torch
 
-    if y.shape == (rows, cols) and y.is_contiguous():
-        if y.dtype == torch.float16:
-            return OUT_F16
-        if y.dtype == torch.float32:
-            return OUT_F32
+    if y is None:
+        y = x.new_empty((rows, cols), dtype=out_dtype or torch.float16)
+    elif y.shape != (rows, cols) or not y.is_contiguous():
+        raise ValueError("y must be a contiguous float16/float32 [%d, %d] tensor" % (rows, cols))
+    if y.dtype == torch.float16:
+        return y, OUT_F16
+    if y.dtype == torch.float32:
+        return y, OUT_F32
     raise ValueError("y must be a contiguous float16/float32 [%d, %d] tensor" % (rows, cols))
 
 
@@ -600,22 +604,23 @@ class PackedExpertsFP8:
         return FMT_FP8
 
 
-def _gemm_experts(y, x, w, offsets, workspace, stream, silu):
+def _gemm_experts(y, x, w, offsets, out_dtype, workspace, stream, silu):
+    """The experts' product into y, or into a new tensor of out_dtype; returns it."""
     import torch
 
     if w.gate_up != silu:
         raise TypeError("gemm_experts takes experts packed without gate_up, gemm_experts_silu_mul with it")
     if x.dtype != torch.float16 or x.dim() != 2 or x.shape[1] != w.K or not x.is_contiguous():
         raise ValueError("x must be a contiguous float16 [T, %d] tensor" % w.K)
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != w.E + 1 or not offsets.is_contiguous():
+    if offsets.dtype != torch.int32 or offsets.shape != (w.E + 1,) or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous int32 [%d] tensor" % (w.E + 1))
-    T = x.shape[0]
-    outputs = w.N // 2 if silu else w.N
-    out = _out_code(y, T, outputs)
+    T, outputs = x.shape[0], w.N // 2 if silu else w.N
+    y, out = _output(y, x, T, outputs, out_dtype)
     ws_ptr, ws_bytes = _ws(workspace)
     d = _device_of(x, y, w.data, w.scale, offsets, workspace)
     _launch("skinny_gemm_experts_silu_mul" if silu else "skinny_gemm_experts", d, stream, w.fmt, x.data_ptr(), T, w.K,
             offsets.data_ptr(), w.E, w.data.data_ptr(), w.scale.data_ptr(), outputs, y.data_ptr(), out, ws_ptr, ws_bytes)
+    return y
 
 
 def gemm_experts_into(y, x, w, offsets, workspace=None, stream=None) -> None:
@@ -623,32 +628,24 @@ def gemm_experts_into(y, x, w, offsets, workspace=None, stream=None) -> None:
     every expert e.  x float16 [T, K], sorted by expert; offsets int32 [E+1] on
     the device; y float16 or float32, preallocated: rows of no expert are left
     as they are.  T may be any number."""
-    _gemm_experts(y, x, w, offsets, workspace, stream, False)
+    _gemm_experts(y, x, w, offsets, None, workspace, stream, False)
 
 
 def gemm_experts(x, w, offsets, out_dtype=None, workspace=None, stream=None):
     """Allocate y [T, N] (float16 unless out_dtype says otherwise): see
     gemm_experts_into.  Rows of no expert are not written."""
-    import torch
-
-    y = x.new_empty((x.shape[0], w.N), dtype=out_dtype or torch.float16)
-    gemm_experts_into(y, x, w, offsets, workspace=workspace, stream=stream)
-    return y
+    return _gemm_experts(None, x, w, offsets, out_dtype, workspace, stream, False)
 
 
 def gemm_experts_silu_mul_into(y, x, w, offsets, workspace=None, stream=None) -> None:
     """y[r, N/2] = silu(gate) * up of the rows' experts (packed with gate_up):
     otherwise as gemm_experts_into."""
-    _gemm_experts(y, x, w, offsets, workspace, stream, True)
+    _gemm_experts(y, x, w, offsets, None, workspace, stream, True)
 
 
 def gemm_experts_silu_mul(x, w, offsets, out_dtype=None, workspace=None, stream=None):
     """Allocate y [T, N/2]: see gemm_experts_silu_mul_into."""
-    import torch
-
-    y = x.new_empty((x.shape[0], w.N // 2), dtype=out_dtype or torch.float16)
-    gemm_experts_silu_mul_into(y, x, w, offsets, workspace=workspace, stream=stream)
-    return y
+    return _gemm_experts(None, x, w, offsets, out_dtype, workspace, stream, True)
 
 
 @dataclasses.dataclass
@@ -675,35 +672,42 @@ class WeightInt8:
         return int(self.codes.shape[1])
 
 
+def _quantize_int8(q, row_scale, x, stream):
+    import torch
+
+    if x.dtype == torch.float16:
+        kind = OUT_F16
+    elif x.dtype == torch.float32:
+        kind = OUT_F32
+    else:
+        kind = None
+    if kind is None or x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous float16/float32 [M, K] tensor")
+    M, K = x.shape
+    if q is None:
+        q = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
+        row_scale = x.new_empty(M, dtype=torch.float32)
+    elif q.shape != x.shape or q.dtype != torch.int8 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous int8 tensor of x's shape")
+    elif row_scale.shape != (M,) or row_scale.dtype != torch.float32 or not row_scale.is_contiguous():
+        raise ValueError("row_scale must be a contiguous float32 [M] tensor")
+    _launch("skinny_quantize_int8", _device_of(x, q, row_scale), stream, x.data_ptr(), kind, M, K, q.data_ptr(),
+            row_scale.data_ptr())
+    return q, row_scale
+
+
 def quantize_int8_into(q, row_scale, x, stream=None) -> None:
     """Rows of x (float16 or float32 [M, K]) to 8-bit integers: row_scale =
     max|x| / 127, q = round(x / row_scale).  q int8 [M, K], row_scale float32 [M]."""
-    import torch
-
-    if x.dim() != 2 or x.dtype not in (torch.float16, torch.float32) or not x.is_contiguous():
-        raise ValueError("x must be a contiguous float16/float32 [M, K] tensor")
-    if q.shape != x.shape or q.dtype != torch.int8 or not q.is_contiguous():
-        raise ValueError("q must be a contiguous int8 tensor of x's shape")
-    M, K = x.shape
-    if row_scale.dtype != torch.float32 or row_scale.dim() != 1 or row_scale.shape[0] != M or not row_scale.is_contiguous():
-        raise ValueError("row_scale must be a contiguous float32 [M] tensor")
-    _launch("skinny_quantize_int8", _device_of(x, q, row_scale), stream, x.data_ptr(),
-            OUT_F32 if x.dtype == torch.float32 else OUT_F16, M, K, q.data_ptr(), row_scale.data_ptr())
+    _quantize_int8(q, row_scale, x, stream)
 
 
 def quantize_int8(x, stream=None):
     """Allocate and return (q int8 [M, K], row_scale float32 [M]): see quantize_int8_into."""
-    import torch
-
-    q = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
-    row_scale = x.new_empty(x.shape[0], dtype=torch.float32)
-    quantize_int8_into(q, row_scale, x, stream=stream)
-    return q, row_scale
+    return _quantize_int8(None, None, x, stream)
 
 
-def gemm_int8_into(y, q, row_scale, w: "WeightInt8", workspace=None, stream=None) -> None:
-    """y[m, n] = (q[m] . w[n]) * row_scale[m] * channel_scale[n], the sum exact
-    (y float16 or float32, preallocated; any number of rows)."""
+def _gemm_int8(y, q, row_scale, w, out_dtype, workspace, stream):
     import torch
 
     N, K = w.codes.shape
@@ -712,20 +716,23 @@ def gemm_int8_into(y, q, row_scale, w: "WeightInt8", workspace=None, stream=None
     M = q.shape[0]
     if row_scale.dtype != torch.float32 or row_scale.shape != (M,) or not row_scale.is_contiguous():
         raise ValueError("row_scale must be a contiguous float32 [M] tensor")
-    out = _out_code(y, M, N)
+    y, out = _output(y, q, M, N, out_dtype)
     ws_ptr, ws_bytes = _ws(workspace)
     _launch("skinny_int8_gemm", _device_of(q, y, row_scale, w.codes, w.channel_scale, workspace), stream, q.data_ptr(),
             row_scale.data_ptr(), M, K, w.codes.data_ptr(), w.channel_scale.data_ptr(), N, y.data_ptr(), out, ws_ptr,
             ws_bytes)
+    return y
+
+
+def gemm_int8_into(y, q, row_scale, w: "WeightInt8", workspace=None, stream=None) -> None:
+    """y[m, n] = (q[m] . w[n]) * row_scale[m] * channel_scale[n], the sum exact
+    (y float16 or float32, preallocated; any number of rows)."""
+    _gemm_int8(y, q, row_scale, w, None, workspace, stream)
 
 
 def gemm_int8(q, row_scale, w: "WeightInt8", out_dtype=None, workspace=None, stream=None):
     """Allocate y [M, N] (float16 unless out_dtype says otherwise): see gemm_int8_into."""
-    import torch
-
-    y = q.new_empty((q.shape[0], w.codes.shape[0]), dtype=out_dtype or torch.float16)
-    gemm_int8_into(y, q, row_scale, w, workspace=workspace, stream=stream)
-    return y
+    return _gemm_int8(None, q, row_scale, w, out_dtype, workspace, stream)
 
 
 def tile_device_error(clear: bool = True) -> int:
@@ -746,19 +753,7 @@ def _prob_dtypes():
     return {torch.float16: PROB_F16, torch.float32: PROB_F32, torch.bfloat16: PROB_BF16}
 
 
-def verify_draft_into(tokens, accepted, target, draft, draft_tokens, uniform, num_drafts=None, stream=None) -> None:
-    """A verify round against the target's probabilities, from given random
-    numbers: draft i of a request is accepted while uniform[i] * q_i(d_i) <
-    p_i(d_i); the next token is drawn from max(p - q, 0) at the first draft that
-    is not accepted, or from the last row of p, with uniform[S].
-
-    target        [B, S+1, V] float32, float16 or bfloat16; unit stride along V
-    draft         [B, S, V] of target's dtype, or None (drafts without a distribution)
-    draft_tokens  int32 [B, S];  uniform  float32 [B, S+1] in [0, 1)
-    num_drafts    int32 [B], or None for S each
-    tokens        int32 [B, S+1]: accepted drafts, the drawn token, then -1
-    accepted      int32 [B]
-    """
+def _verify_draft(tokens, accepted, target, draft, draft_tokens, uniform, num_drafts, stream):
     import torch
 
     kind = _prob_dtypes().get(target.dtype)
@@ -786,21 +781,36 @@ def verify_draft_into(tokens, accepted, target, draft, draft_tokens, uniform, nu
         raise ValueError("uniform must be a contiguous float32 [%d, %d] tensor" % shape)
     if num_drafts is not None and (num_drafts.dtype != i32 or num_drafts.shape != (B,) or not num_drafts.is_contiguous()):
         raise ValueError("num_drafts must be a contiguous int32 [%d] tensor" % B)
-    if tokens.dtype != i32 or tokens.shape != shape or not tokens.is_contiguous():
+    if tokens is None:
+        tokens = torch.empty_like(uniform, dtype=i32)
+        accepted = uniform.new_empty(B, dtype=i32)
+    elif tokens.dtype != i32 or tokens.shape != shape or not tokens.is_contiguous():
         raise ValueError("tokens must be a contiguous int32 [%d, %d] tensor" % shape)
-    if accepted.dtype != i32 or accepted.shape != (B,) or not accepted.is_contiguous():
+    elif accepted.dtype != i32 or accepted.shape != (B,) or not accepted.is_contiguous():
         raise ValueError("accepted must be a contiguous int32 [%d] tensor" % B)
     d = _device_of(target, draft, draft_tokens, uniform, num_drafts, tokens, accepted)
     _launch("skinny_verify_draft", d, stream, target.data_ptr(), target_b, target_s, draft_ptr, draft_b, draft_s, kind,
             draft_tokens.data_ptr() if S else None, uniform.data_ptr(),
             num_drafts.data_ptr() if num_drafts is not None else None, B, S, V, tokens.data_ptr(), accepted.data_ptr())
+    return tokens, accepted
+
+
+def verify_draft_into(tokens, accepted, target, draft, draft_tokens, uniform, num_drafts=None, stream=None) -> None:
+    """A verify round against the target's probabilities, from given random
+    numbers: draft i of a request is accepted while uniform[i] * q_i(d_i) <
+    p_i(d_i); the next token is drawn from max(p - q, 0) at the first draft that
+    is not accepted, or from the last row of p, with uniform[S].
+
+    target        [B, S+1, V] float32, float16 or bfloat16; unit stride along V
+    draft         [B, S, V] of target's dtype, or None (drafts without a distribution)
+    draft_tokens  int32 [B, S];  uniform  float32 [B, S+1] in [0, 1)
+    num_drafts    int32 [B], or None for S each
+    tokens        int32 [B, S+1]: accepted drafts, the drawn token, then -1
+    accepted      int32 [B]
+    """
+    _verify_draft(tokens, accepted, target, draft, draft_tokens, uniform, num_drafts, stream)
 
 
 def verify_draft(target, draft, draft_tokens, uniform, num_drafts=None, stream=None):
     """Allocate and return (tokens int32 [B, S+1], accepted int32 [B]): see verify_draft_into."""
-    import torch
-
-    tokens = torch.empty_like(uniform, dtype=torch.int32, memory_format=torch.contiguous_format)
-    accepted = uniform.new_empty(uniform.shape[0], dtype=torch.int32)
-    verify_draft_into(tokens, accepted, target, draft, draft_tokens, uniform, num_drafts, stream=stream)
-    return tokens, accepted
+    return _verify_draft(None, None, target, draft, draft_tokens, uniform, num_drafts, stream)

@@ -637,9 +637,10 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
     bool mine = false;
     Producer<FMT, TN> producer;
     if (!C::kInt8 && warp == 0 && ptx::elect_one()) {
-        // the warp that made the schedule fills its ring before the CTA is ready
+        // the warp that made the schedule starts on its ring before the CTA is
+        // ready: with two slots, as a copy takes ~160 ns to issue
         producer.begin(s, p);
-        producer.produce(sm, r, issued, C::kWStages, s, p, &w_map, &w_map2, leader);
+        producer.produce(sm, r, issued, 2, s, p, &w_map, &w_map2, leader);
     }
     __syncwarp();
     ptx::tc_fence_before();
