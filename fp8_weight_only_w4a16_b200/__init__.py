@@ -477,6 +477,11 @@ def _launch(name, d, stream, *args) -> None:
         raise SkinnyError(st, name)
 
 
+def _given(*outputs):
+    if any(t is None for t in outputs):
+        raise ValueError("the output tensors must be given")
+
+
 def _ws(workspace):
     if workspace is None:
         return None, 0
@@ -628,6 +633,7 @@ def gemm_experts_into(y, x, w, offsets, workspace=None, stream=None) -> None:
     every expert e.  x float16 [T, K], sorted by expert; offsets int32 [E+1] on
     the device; y float16 or float32, preallocated: rows of no expert are left
     as they are.  T may be any number."""
+    _given(y)
     _gemm_experts(y, x, w, offsets, None, workspace, stream, False)
 
 
@@ -640,6 +646,7 @@ def gemm_experts(x, w, offsets, out_dtype=None, workspace=None, stream=None):
 def gemm_experts_silu_mul_into(y, x, w, offsets, workspace=None, stream=None) -> None:
     """y[r, N/2] = silu(gate) * up of the rows' experts (packed with gate_up):
     otherwise as gemm_experts_into."""
+    _given(y)
     _gemm_experts(y, x, w, offsets, None, workspace, stream, True)
 
 
@@ -699,6 +706,7 @@ def _quantize_int8(q, row_scale, x, stream):
 def quantize_int8_into(q, row_scale, x, stream=None) -> None:
     """Rows of x (float16 or float32 [M, K]) to 8-bit integers: row_scale =
     max|x| / 127, q = round(x / row_scale).  q int8 [M, K], row_scale float32 [M]."""
+    _given(q, row_scale)
     _quantize_int8(q, row_scale, x, stream)
 
 
@@ -727,6 +735,7 @@ def _gemm_int8(y, q, row_scale, w, out_dtype, workspace, stream):
 def gemm_int8_into(y, q, row_scale, w: "WeightInt8", workspace=None, stream=None) -> None:
     """y[m, n] = (q[m] . w[n]) * row_scale[m] * channel_scale[n], the sum exact
     (y float16 or float32, preallocated; any number of rows)."""
+    _given(y)
     _gemm_int8(y, q, row_scale, w, None, workspace, stream)
 
 
@@ -808,6 +817,7 @@ def verify_draft_into(tokens, accepted, target, draft, draft_tokens, uniform, nu
     tokens        int32 [B, S+1]: accepted drafts, the drawn token, then -1
     accepted      int32 [B]
     """
+    _given(tokens, accepted)
     _verify_draft(tokens, accepted, target, draft, draft_tokens, uniform, num_drafts, stream)
 
 

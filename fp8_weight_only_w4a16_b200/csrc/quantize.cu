@@ -61,8 +61,10 @@ __global__ void __launch_bounds__(1024)
              float* __restrict__ row_scale)
 {
     __shared__ uint32_t part[32];
-    ptx::pdl_launch_dependents();
+    // The next kernel may start once this one has seen the previous one's end:
+    // what it reads early was then written two kernels ago at the latest.
     ptx::pdl_wait_prior_grid();
+    ptx::pdl_launch_dependents();
     const int r = threadIdx.x / threads_per_row, t = threadIdx.x % threads_per_row;
     const int64_t m = (int64_t)blockIdx.x * (blockDim.x / threads_per_row) + r;
     const bool live = m < M;

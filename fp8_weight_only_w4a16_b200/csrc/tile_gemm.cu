@@ -44,6 +44,7 @@ constexpr int kFmtInt8 = 2;           // next to SKINNY_FMT_NVFP4 and SKINNY_FMT
 constexpr int kMaxExperts = SKINNY_MAX_EXPERTS;
 constexpr int kMaxDevices = 64;
 constexpr int kSlotWords = kRows * 256;   // one CTA's partial tile in the workspace
+constexpr int kAheadBlocks = 4;           // int8 weight blocks prefetched before the previous kernel is done
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // Bits of g_tile_error: which bounded wait gave up.
@@ -614,7 +615,8 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
     __syncwarp();
     const int rank = C::kPair ? (int)ptx::cluster_rank() : 0;
     const bool leader = rank == 0;
-    ptx::pdl_launch_dependents();
+    // The next kernel may start once this one has seen the previous one's end
+    // (what it reads early was then written two kernels ago at the latest).
     if constexpr (C::kInt8) {
         // The schedule needs nothing of the previous kernel: only the roles
         // that touch its results wait for it.
@@ -627,6 +629,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         }
     } else {
         ptx::pdl_wait_prior_grid();
+        ptx::pdl_launch_dependents();
         if (warp == 0) make_schedule<TN, C::kPair>(s, p);
     }
     Ring r;            // position of a single-thread role, and how much it has issued
@@ -655,7 +658,16 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         // ---- W producer
         if (ptx::elect_one()) {
             mine = true;
-            if (C::kInt8) producer.begin(s, p);
+            if constexpr (C::kInt8) {
+                // Until the previous kernel is done, the weights are only brought into L2: they
+                // are a plain tensor that it may have written.
+                Walk<TN, C::kPair> ahead(s, p);
+                if (ahead.next(g) && g.row_tile < p.G)
+                    for (int k = g.k0; k < g.k1 && k < g.k0 + kAheadBlocks; ++k)
+                        ptx::tma_prefetch_2d(C::kW3d ? &w_map2 : &w_map, k * kBlockK, g.row_tile * kRows);
+                ptx::pdl_wait_prior_grid();
+                producer.begin(s, p);
+            }
             producer.produce(sm, r, issued, 0x7FFFFFFF, s, p, &w_map, &w_map2, leader);
         }
     } else if (warp == 1) {
@@ -664,7 +676,10 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             mine = true;
             bool ok = true;
             const uint64_t pol = TN <= 32 ? ptx::policy_evict_last() : ptx::policy_evict_normal();
-            if (C::kInt8) ptx::pdl_wait_prior_grid();
+            if (C::kInt8) {
+                ptx::pdl_wait_prior_grid();
+                ptx::pdl_launch_dependents();
+            }
             constexpr int kChunkK = kBlockK / C::kChunksPerBlock;
             const int whole = p.K / kChunkK;      // pieces that lie within K entirely
             while (ok && walk.next(g)) {

@@ -254,8 +254,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify(const __grid_constant__ Pa
 
     // Before the first write to another CTA's shared memory, all have to run.
     auto started = cluster.barrier_arrive();
-    ptx::pdl_launch_dependents();
+    // The next kernel may start once this one has seen the previous one's end:
+    // what it reads early was then written two kernels ago at the latest.
     ptx::pdl_wait_prior_grid();
+    ptx::pdl_launch_dependents();
     const T* target = static_cast<const T*>(a.target) + b * a.target_b;
     const T* draft = a.draft ? static_cast<const T*>(a.draft) + b * a.draft_b : nullptr;
     const int32_t* drafted = a.draft_tokens + b * a.S;

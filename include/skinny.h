@@ -333,7 +333,8 @@ int skinny_debug_static_workspace_address(void** addr);
  *
  * These calls take any number of rows, from one to SKINNY_MAX_TOKENS, and run
  * on the tcgen05 tensor cores.  Conventions as above (asynchronous on
- * `stream`, caller-owned buffers, programmatic dependent launch), and:
+ * `stream`, caller-owned buffers, programmatic dependent launch: these calls
+ * read and write nothing before the previous kernel is done), and:
  *   - T = 0 (M = 0) returns SKINNY_OK and does nothing.
  *   - The workspace (device, 16-byte aligned) is optional, has
  *     skinny_tile_workspace_bytes() bytes on every shape, and must be
@@ -420,9 +421,9 @@ int skinny_quantize_int8(const void* x, int in_dtype, int64_t M, int64_t K, void
  * The sum is exact; it is rounded to FP32, multiplied by row_scale[m], then by
  * channel_scale[n], and rounded to the output type.
  *   q              device int8 [M][K], 16-byte aligned.
- *   w              device int8 [N][K] as it is (no packing), 16-byte aligned;
- *                  like packed weights it must not be written by the kernel
- *                  launched just before.
+ *   w              device int8 [N][K] as it is (no packing), 16-byte aligned.
+ *                  It may be written by the kernel launched just before (the
+ *                  call only prefetches it into L2 until that is done).
  *   row_scale      device float[M];  channel_scale  device float[N].
  *   y              device [M][N], FP16 or FP32 per out_dtype, aligned to its type.
  * UNSUPPORTED for K > SKINNY_MAX_INT8_K. */
