@@ -178,6 +178,23 @@ __device__ __forceinline__ uint16_t lds16(uint32_t addr)
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Loads of what the previous kernel may have written.  They are coherent, not
+// read-only loads (the data changes in this kernel's lifetime, and read-only
+// loads were moved in front of the wait above); they can be scheduled freely
+// behind it because their address comes from after_wait().
+template <typename T>
+__device__ __forceinline__ const T* after_wait(const T* p)
+{
+    asm volatile("" : "+l"(p)::"memory");
+    return p;
+}
+__device__ __forceinline__ uint4 ld_global_v4(const uint4* p)
+{
+    uint4 v;
+    asm("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 // Split-K partial sums travel between CTAs through global memory with
 // volatile (relaxed, system-scope) accesses: the finisher polls a slot until
 // the publisher's value appears, so neither side may use a weak access that

@@ -619,8 +619,8 @@ __device__ __forceinline__ void load_b(const uint16_t* xrow, bool valid, int kb,
     uint4 x0 = make_uint4(0, 0, 0, 0), x1 = make_uint4(0, 0, 0, 0);
     if (valid && kb < K) {
         const uint4* xp = reinterpret_cast<const uint4*>(xrow + kb);
-        x0 = __ldg(xp);
-        x1 = __ldg(xp + 1);
+        x0 = ptx::ld_global_v4(xp);
+        x1 = ptx::ld_global_v4(xp + 1);
     }
     bx[0] = x0.x; bx[1] = x0.y; bx[2] = x0.z; bx[3] = x0.w;
     bx[4] = x1.x; bx[5] = x1.y; bx[6] = x1.z; bx[7] = x1.w;
@@ -778,7 +778,7 @@ __device__ void consume(const Params& p, uint8_t* smem, uint64_t* full, uint64_t
     int nc = c;                                            // K tile whose activations are fetched next
     int ng = g;                                            // ... and its row tile
     int nm = member_of_row<GR>(p, ng);                     // ... and its GEMM
-    const uint16_t* xbase = p.mem[nm].x;
+    const uint16_t* xbase = ptx::after_wait(p.mem[nm].x);
     const uint32_t smem32 = ptx::smem_addr(smem);
     int* released = reinterpret_cast<int*>(smem + S::kCountOff);
     // Fused argmax: this lane's best key per token it holds (tokens 8nb + 2t + e).
@@ -830,7 +830,7 @@ __device__ void consume(const Params& p, uint8_t* smem, uint64_t* full, uint64_t
         if (nc == 0) {
             nc = p.C;
             if constexpr (GR) {
-                if (--ng < p.mem[nm].g_begin && nm > 0) xbase = p.mem[--nm].x;
+                if (--ng < p.mem[nm].g_begin && nm > 0) xbase = ptx::after_wait(p.mem[--nm].x);
             }
         }
         --nc;
