@@ -455,11 +455,11 @@ def device_error(clear: bool = True) -> int:
 def _device_of(x, *others) -> int:
     """The index of x's CUDA device, which every other tensor must be on."""
     d = x.get_device()
-    if d < 0:
-        raise ValueError("tensors on a CUDA device expected, got %s" % x.device)
     for t in others:
         if t is not None and t.get_device() != d:
             raise ValueError("tensors on one device expected: %s and %s" % (x.device, t.device))
+    if d < 0:
+        raise ValueError("tensors on a CUDA device expected, got %s" % x.device)
     return d
 
 
@@ -718,16 +718,19 @@ def quantize_int8(x, stream=None):
 def _gemm_int8(y, q, row_scale, w, out_dtype, workspace, stream):
     import torch
 
-    N, K = w.codes.shape
-    if q.dtype != torch.int8 or q.dim() != 2 or q.shape[1] != K or not q.is_contiguous():
+    codes, channel_scale = w.codes, w.channel_scale
+    N, K = codes.shape
+    if q.dtype != torch.int8 or q.dim() != 2 or not q.is_contiguous():
         raise ValueError("q must be a contiguous int8 [M, %d] tensor" % K)
-    M = q.shape[0]
+    M, k = q.shape
+    if k != K:
+        raise ValueError("q must be a contiguous int8 [M, %d] tensor" % K)
     if row_scale.dtype != torch.float32 or row_scale.shape != (M,) or not row_scale.is_contiguous():
         raise ValueError("row_scale must be a contiguous float32 [M] tensor")
     y, out = _output(y, q, M, N, out_dtype)
     ws_ptr, ws_bytes = _ws(workspace)
-    _launch("skinny_int8_gemm", _device_of(q, y, row_scale, w.codes, w.channel_scale, workspace), stream, q.data_ptr(),
-            row_scale.data_ptr(), M, K, w.codes.data_ptr(), w.channel_scale.data_ptr(), N, y.data_ptr(), out, ws_ptr,
+    _launch("skinny_int8_gemm", _device_of(q, y, row_scale, codes, channel_scale, workspace), stream, q.data_ptr(),
+            row_scale.data_ptr(), M, K, codes.data_ptr(), channel_scale.data_ptr(), N, y.data_ptr(), out, ws_ptr,
             ws_bytes)
     return y
 
@@ -792,7 +795,7 @@ def _verify_draft(tokens, accepted, target, draft, draft_tokens, uniform, num_dr
         raise ValueError("num_drafts must be a contiguous int32 [%d] tensor" % B)
     if tokens is None:
         tokens = torch.empty_like(uniform, dtype=i32)
-        accepted = uniform.new_empty(B, dtype=i32)
+        accepted = tokens.new_empty(B)
     elif tokens.dtype != i32 or tokens.shape != shape or not tokens.is_contiguous():
         raise ValueError("tokens must be a contiguous int32 [%d, %d] tensor" % shape)
     elif accepted.dtype != i32 or accepted.shape != (B,) or not accepted.is_contiguous():

@@ -1107,7 +1107,8 @@ int launch(Params p, const void* x, const void* w, int grid, cudaStream_t stream
     CUtensorMap xm, xm2, wm, wm2;
     if (!make_map(&xm, x, !C::kInt8, p.T, p.K, C::kBox, C::kX3d ? C::kChunks : 1)) return SKINNY_ERR_CUDA;
     wm = wm2 = xm2 = xm;
-    if (C::kX3d && !make_map(&xm2, x, !C::kInt8, p.T, p.K, C::kBox, 1)) return SKINNY_ERR_CUDA;
+    // (read only where K ends inside a block)
+    if (C::kX3d && p.K % kBlockK != 0 && !make_map(&xm2, x, !C::kInt8, p.T, p.K, C::kBox, 1)) return SKINNY_ERR_CUDA;
     if (C::kInt8) {
         if (!make_map(&wm, w, false, p.N, p.K, kRows, C::kW3d ? 2 : 1)) return SKINNY_ERR_CUDA;
         if (C::kW3d && !make_map(&wm2, w, false, p.N, p.K, kRows, 1)) return SKINNY_ERR_CUDA;
