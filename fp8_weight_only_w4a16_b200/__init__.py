@@ -1,6 +1,8 @@
 """B200-native weight-only skinny GEMM: y[M,N] = x[M,K] . W^T, M = 1..16,
 with W kept in HBM as NVFP4 (E2M1 codes + UE4M3 per-16 scales + FP32 global)
-or FP8 E4M3 (+ FP32 per output channel), FP16 activations, FP32 accumulation.
+or FP8 E4M3 (+ FP32 per output channel), FP16 activations, FP32 accumulation;
+products for any number of tokens, grouped by expert (the same formats) or in
+8-bit integers; and the verification of drafted tokens.
 
 This module is a thin ctypes binding over ``libskinny.so`` (whose C ABI is
 ``include/skinny.h``): it turns numpy arrays and torch tensors into pointers,

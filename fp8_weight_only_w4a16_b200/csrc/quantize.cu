@@ -4,7 +4,9 @@
 //
 // One group of warps per row holds the row in registers between the maximum
 // and the rounding, so x is read once (2 or 4 bytes an element) and q written
-// once (1 byte).  Bound by HBM, or by latency for a few rows.
+// once (1 byte).  Bound by HBM, or by latency for a few rows.  Rounding an
+// exact quotient costs nothing beside that: the division in 64 bits runs for
+// about one element in 16,000.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -18,38 +20,85 @@ namespace {
 constexpr int kVec = 8;            // elements a thread reads at once
 constexpr int kMaxVecs = 4;        // vectors a thread keeps in registers
 
+// Eight elements as they lie in memory.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* x, int64_t i, float (&v)[kVec])
-{
-    if constexpr (F32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + i);
-        const float4 a = p[0], b = p[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-        const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const __half*>(x) + i);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Raw {
+    uint4 w[F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* x, int64_t i)
+    {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + i * (F32 ? 4 : 2));
+        w[0] = p[0];
+        if (F32) w[F32 ? 1 : 0] = p[1];
+    }
+    __device__ __forceinline__ void floats(float (&v)[kVec]) const
+    {
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-            v[2 * j] = f.x;
-            v[2 * j + 1] = f.y;
+        for (int j = 0; j < kVec; ++j) {
+            if (F32) {
+                v[j] = __uint_as_float(u[j]);
+            } else if (j % 2 == 0) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j / 2]));
+                v[j] = f.x;
+                v[j + 1] = f.y;
+            }
         }
     }
+    // The largest magnitude as FP32 bits: ordered like the values, NaN above infinity.
+    __device__ __forceinline__ uint32_t top() const
+    {
+        const uint32_t* u = reinterpret_cast<const uint32_t*>(w);
+        if constexpr (F32) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) m = max(m, u[j] & 0x7FFFFFFFu);
+            return m;
+        } else {
+            // two halves at a time, as 16-bit whole numbers
+            uint32_t m = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu),
+                                  __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
+            m = max(m & 0xFFFFu, m >> 16);
+            return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+        }
+    }
+};
+
+// x / scale to the nearest whole number, ties to even, of the exact quotient:
+// the division in 64 bits, whose own rounding cannot cross the middle of two
+// whole numbers (x has 24 bits, the middle times the scale 32).
+__device__ __noinline__ int exact_quotient(float x, float scale)
+{
+    const double q = rint((double)x / (double)scale);
+    return (int)fmin(fmax(q, -127.0), 127.0);
 }
 
-// x / scale to the nearest whole number, ties to even, as if the quotient were
-// exact.  x * (1 / scale) in FP32 is at most 127 * 2^-22 off (the reciprocal,
-// the product and the scale's own range), so only quotients that close to the
-// middle of two whole numbers need the division in 64 bits, whose own rounding
-// cannot cross the middle: x has 24 bits and the middle times the scale 32.
-// A scale whose reciprocal overflows comes this way too (t is inf or NaN).
-__device__ __forceinline__ int round_quotient(float x, float scale, float inv)
+// Eight quotients as bytes.  fma(x, 1 / scale, 1.5 * 2^23) rounds the product to
+// a whole number, which its low byte holds.  The reciprocal is at most 2^-24 of
+// itself off, so the product is off by less than 127 * 2^-22, and only a
+// quotient that close to the middle of two whole numbers can have gone wrong:
+// then (one vector in some 2000) the eight are divided in 64 bits.  `normal`:
+// the scale is a normal number, so that its reciprocal is one.
+__device__ __forceinline__ uint2 quotients(const float (&x)[kVec], float scale, float inv, bool normal)
 {
-    const float t = x * inv;
-    float q = rintf(t);
-    if (!(fabsf(fabsf(t - q) - 0.5f) > 127.f / (1 << 22))) q = (float)rint((double)x / (double)scale);
-    return (int)fminf(fmaxf(q, -127.f), 127.f);
+    constexpr float kMagic = 12582912.f;
+    uint32_t b[kVec];
+    float off = 0.f;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+        const float r = __fmaf_rn(x[j], inv, kMagic);
+        off = fmaxf(off, fabsf(__fmaf_rn(x[j], inv, kMagic - r)));
+        b[j] = __float_as_uint(r);
+    }
+    if (!normal || off > 0.5f - 127.f / (1 << 22)) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) b[j] = (uint32_t)exact_quotient(x[j], scale);
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        w[h] = __byte_perm(__byte_perm(b[4 * h], b[4 * h + 1], 0x0040), __byte_perm(b[4 * h + 2], b[4 * h + 3], 0x0040),
+                           0x5410);
+    return make_uint2(w[0], w[1]);
 }
 
 // threads_per_row (a multiple of 32) threads work on a row; a block holds
@@ -71,24 +120,21 @@ __global__ void __launch_bounds__(1024)
     const int64_t row = m * K;
     const int n = K / kVec;
 
-    float v[KEEP ? kMaxVecs : 1][kVec];
-    uint32_t top = 0;    // |x| as bits: ordered like the values, NaN above infinity
+    Raw<F32> v[KEEP ? kMaxVecs : 1];
+    uint32_t top = 0;
     if (live) {
         if constexpr (KEEP) {
 #pragma unroll
-            for (int i = 0; i < kMaxVecs; ++i) {
-                const int at = t + i * threads_per_row;
-                if (at < n) {
-                    load8<F32>(x, row + (int64_t)at * kVec, v[i]);
+            for (int i = 0; i < kMaxVecs; ++i)
+                if (t + i * threads_per_row < n) v[i].load(x, row + (int64_t)(t + i * threads_per_row) * kVec);
 #pragma unroll
-                    for (int j = 0; j < kVec; ++j) top = max(top, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
-                }
-            }
+            for (int i = 0; i < kMaxVecs; ++i)
+                if (t + i * threads_per_row < n) top = max(top, v[i].top());
         } else {
+#pragma unroll 4
             for (int at = t; at < n; at += threads_per_row) {
-                load8<F32>(x, row + (int64_t)at * kVec, v[0]);
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) top = max(top, __float_as_uint(v[0][j]) & 0x7FFFFFFFu);
+                v[0].load(x, row + (int64_t)at * kVec);
+                top = max(top, v[0].top());
             }
         }
     }
@@ -104,15 +150,13 @@ __global__ void __launch_bounds__(1024)
     const float scale = finite ? __fdiv_rn(__uint_as_float(top), 127.f) : __uint_as_float(0x7FC00000u);
     const float inv = __fdiv_rn(1.f, scale);
     const bool zero = !(scale > 0.f);      // a row of zeros, or one that is not finite
+    const bool normal = scale >= 1.17549435e-38f;
     if (t == 0) row_scale[m] = scale;
-    auto put = [&](int at, const float (&f)[kVec]) {
-        uint32_t w[2] = {0, 0};
-        if (!zero) {
-#pragma unroll
-            for (int j = 0; j < kVec; ++j)
-                w[j / 4] |= (uint32_t)(uint8_t)(int8_t)round_quotient(f[j], scale, inv) << (8 * (j % 4));
-        }
-        *reinterpret_cast<uint2*>(q + row + (int64_t)at * kVec) = make_uint2(w[0], w[1]);
+    auto put = [&](int at, const Raw<F32>& raw) {
+        float f[kVec];
+        raw.floats(f);
+        *reinterpret_cast<uint2*>(q + row + (int64_t)at * kVec) =
+            zero ? make_uint2(0, 0) : quotients(f, scale, inv, normal);
     };
     if constexpr (KEEP) {
 #pragma unroll
@@ -121,8 +165,9 @@ __global__ void __launch_bounds__(1024)
             if (at < n) put(at, v[i]);
         }
     } else {
+#pragma unroll 2
         for (int at = t; at < n; at += threads_per_row) {
-            load8<F32>(x, row + (int64_t)at * kVec, v[0]);
+            v[0].load(x, row + (int64_t)at * kVec);
             put(at, v[0]);
         }
     }

@@ -4,28 +4,41 @@
 //             expert, ragged), W_e packed NVFP4 or FP8, x FP16;
 //   int8:     y[m][n] = (sum_k q[m][k] c[n][k]) * row_scale[m] * channel_scale[n].
 //
-// One kernel serves both.  The weights are the 128 rows of the matrix
-// instruction and the tokens its columns, so one token costs 16 columns and
-// a long batch 256, and the same kernel runs from one row to many thousands.
-// Per CTA (one per SM, persistent):
+// One kernel serves both.  The weights are the rows of the matrix instruction
+// (128, or 256 of a pair of CTAs) and the tokens its columns, so one token
+// costs 16 columns and a long batch 192 (int8: 256), and the same kernel runs
+// from one row to many thousands.  Per CTA (one per SM, persistent):
 //
 //   W producer   one thread, bulk copies of packed 128 x 128 blocks (experts)
 //                or tiled TMA boxes of the plain [N][K] matrix (int8);
 //   x producer   one thread, tiled TMA boxes of the activations;
-//   decoders     eight warps (experts only): a thread owns one weight row of
-//                the block and writes its 64 decoded FP16 values straight
-//                into tensor memory, from where the matrix instruction reads
-//                operand A.  The decoded weights never pass through shared
-//                memory, whose bandwidth would not carry them at the rate
-//                the codes arrive from HBM (2 bytes written and 2 read per
-//                weight against 0.56 bytes of HBM traffic).
+//   decoders     two groups of four warps (experts only): a thread owns one
+//                weight row of a block and writes its decoded FP16 values
+//                straight into tensor memory, from where the matrix
+//                instruction reads operand A.  The decoded weights never pass
+//                through shared memory, whose bandwidth would not carry them
+//                at the rate the codes arrive from HBM (2 bytes written and 2
+//                read per weight against 0.56 bytes of HBM traffic);
 //   MMA          one thread issues tcgen05.mma into FP32 (int8: S32) accumulators;
-//   epilogue     four warps: a thread owns one output channel.
+//   epilogue     four or eight warps: a thread owns one output channel.
 //
 // Every product is exact (e2m1 * ue4m3 and e4m3 fit FP16, s8 * s8 fits S32);
 // the FP32 sums round as the tensor core's accumulator does, the S32 sums not
 // at all.  The scales are applied to the finished sum in FP32, and the output
 // is rounded once.
+//
+// What bounds it, and what it measured on a B200 (6.46 TB/s copy, 1708 TFLOP/s
+// bf16; back-to-back launches in a CUDA graph, weights from HBM):
+//   few rows, FP8     HBM: 64 rows over 128 experts of 5120 x 1408, 49 to 53 us
+//                     (5.9 to 6.4 TB/s).
+//   few rows, NVFP4   the decoders: 64 rows over 128 experts of 2816 x 5120,
+//                     65 us (5.4 TB/s); a block takes its two groups ~430
+//                     clocks, HBM ~390.
+//   many rows         the tensor cores under the power limit: 16387 rows over
+//                     32 experts of 2816 x 5120, 358 to 385 us (1.23 to 1.32
+//                     PFLOP/s); int8 2048 x 34816 x 5120, 290 to 330 us (2.2
+//                     to 2.5 POP/s, at 1.1 to 1.3 GHz).
+//   one token         latency: eight experts of 2816 x 2048 (23 MB) 13 us.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -84,11 +97,11 @@ struct Params {
 constexpr int at_most(int a, int b) { return a < b ? a : b; }
 
 // A step is what one turn of every role handles: two K blocks of a narrow
-// tile, one of a wide one.  Per step the MMA thread waits for one barrier,
-// issues and commits to one barrier: each further wait or commit costs it
-// some hundred clocks (its code competes with the decoders' for the
-// instruction caches), and a narrow step has to fit in the ~800 clocks in
-// which its weights arrive from HBM.
+// tile, one of a wide one.  Every turn of a decoder or of the MMA thread costs
+// it some hundred clocks of waits, arrivals and commits beside its work, and a
+// narrow step has to fit in the ~780 clocks in which its weights arrive from
+// HBM: steps of half the size measured 93 us for 71 (64 rows, 128 experts) and
+// 484 us for 396 (16387 rows).
 template <int FMT, int TN>
 struct Cfg {
     static constexpr bool kInt8 = FMT == kFmtInt8;
@@ -723,6 +736,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         // ---- MMA: one thread issues (a pair's: the leader's)
         if (leader && ptx::elect_one()) {
             mine = true;
+            if (C::kInt8) ptx::pdl_wait_prior_grid();      // so that no bounded wait runs against another kernel
             Ring dr;
             constexpr uint32_t kXStep = C::kXBytes >> 4, kXChunkStep = C::kChunkBytes >> 4;
             constexpr uint32_t kAStep = C::kInt8 ? C::kWBytes >> 4 : 64 * C::kStepBlocks;
