@@ -985,8 +985,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
     if (warp == 2) ptx::tmem_free_all<C::kPair>(tmem);
 }
 
-// Packs experts on the device: one thread per 16 bytes of a block's codes (or,
-// NVFP4, per row and half of its block scales).
+// Packs experts on the device: a CTA per block, a thread per 16 bytes of its codes.
 __global__ void pack_experts(int fmt, const uint8_t* codes, const uint8_t* scales, int N, int K, int outputs, int G,
                              int Cb, int gate_up, uint8_t* packed)
 {
@@ -1000,23 +999,29 @@ __global__ void pack_experts(int fmt, const uint8_t* codes, const uint8_t* scale
     const int row_bytes = fmt == SKINNY_FMT_NVFP4 ? K / 2 : K;
     const int chunk_bytes = fmt == SKINNY_FMT_NVFP4 ? 64 : 128;
     const int words = chunk_bytes / 16;
-    for (int i = threadIdx.x; i < kRows * (words + 1); i += blockDim.x) {
-        const int r = i % kRows, j = i / kRows;
+    // the source row of packed row r, or -1 past the outputs
+    auto source = [&](int r) -> int64_t {
         const int l = r & 31;
         const int o = gate_up ? g * 64 + (r / 32) * 16 + (l & 15) : g * kRows + r;
-        const int64_t n = o + (gate_up && l >= 16 ? outputs : 0);
-        if (j < words) {
-            for (int b = 0; b < 16; ++b) {
-                const int at = c * chunk_bytes + j * 16 + b;
-                out[(j * kRows + r) * 16 + b] =
-                    o < outputs && at < row_bytes ? codes[(e * N + n) * row_bytes + at] : 0;
-            }
-        } else if (fmt == SKINNY_FMT_NVFP4) {
-            for (int b = 0; b < 8; ++b) {
-                const int at = c * 8 + b;
-                out[kNvfp4BlockScales + r * 8 + b] =
-                    o < outputs && at < K / 16 ? scales[(e * N + n) * (K / 16) + at] : 0;
-            }
+        return o < outputs ? e * N + o + (gate_up && l >= 16 ? outputs : 0) : -1;
+    };
+    // neighbouring threads read along a row; rows are multiples of 8 bytes
+    for (int i = threadIdx.x; i < kRows * words; i += blockDim.x) {
+        const int j = i % words, r = i / words, at = c * chunk_bytes + j * 16;
+        const int64_t n = source(r);
+        uint2 v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            v[h] = n >= 0 && at + 8 * h < row_bytes
+                       ? *reinterpret_cast<const uint2*>(codes + n * row_bytes + at + 8 * h)
+                       : make_uint2(0, 0);
+        *reinterpret_cast<uint4*>(out + (j * kRows + r) * 16) = make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
+    }
+    if (fmt == SKINNY_FMT_NVFP4) {
+        for (int i = threadIdx.x; i < kRows * 8; i += blockDim.x) {
+            const int b = i % 8, r = i / 8, at = c * 8 + b;
+            const int64_t n = source(r);
+            out[kNvfp4BlockScales + i] = n >= 0 && at < K / 16 ? scales[n * (K / 16) + at] : 0;
         }
     }
 }
@@ -1250,7 +1255,7 @@ extern "C" int skinny_pack_experts(int fmt, const void* codes, const void* scale
     int64_t G, C;
     if (!experts_shape(fmt, E, N, K, gate_up, &G, &C)) return SKINNY_ERR_INVALID_ARG;
     if (!codes || !w_packed || (fmt == SKINNY_FMT_NVFP4 && !scales)) return SKINNY_ERR_INVALID_ARG;
-    if (!aligned(w_packed, 16)) return SKINNY_ERR_ALIGNMENT;
+    if (!aligned(w_packed, 16) || !aligned(codes, 8)) return SKINNY_ERR_ALIGNMENT;
     if (E * G >= 65536 * int64_t(1024)) return SKINNY_ERR_UNSUPPORTED;
     // block index = x + y * gridDim.x over exactly E * G * C blocks
     int64_t gx = E * G * C, gy = 1;

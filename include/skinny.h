@@ -365,7 +365,8 @@ int skinny_tile_workspace_bytes(size_t* bytes);
 size_t skinny_experts_packed_bytes(int fmt, int64_t E, int64_t N, int64_t K, int gate_up);
 
 /* Packs experts ON THE DEVICE, once, when a model is loaded.
- *   codes     device: NVFP4 [E][N][K/2] (low nibble = even k), FP8 [E][N][K] E4M3.
+ *   codes     device: NVFP4 [E][N][K/2] (low nibble = even k), FP8 [E][N][K]
+ *             E4M3; 8-byte aligned.
  *   scales    device, NVFP4: [E][N][K/16] UE4M3; FP8: ignored.
  *   gate_up   non-zero: rows 0..N/2-1 are gate and N/2..N-1 up, packed for
  *             skinny_gemm_experts_silu_mul.

@@ -127,6 +127,7 @@ def test_packed_sizes_and_refusals():
     assert lib.skinny_pack_experts(0, None, ALIGNED, 1, 128, 128, 0, ALIGNED, None) == sk.ERR_INVALID_ARG
     assert lib.skinny_pack_experts(0, ALIGNED, None, 1, 128, 128, 0, ALIGNED, None) == sk.ERR_INVALID_ARG
     assert lib.skinny_pack_experts(0, ALIGNED, ALIGNED, 1, 128, 128, 0, ALIGNED + 4, None) == sk.ERR_ALIGNMENT
+    assert lib.skinny_pack_experts(0, ALIGNED + 4, ALIGNED, 1, 128, 128, 0, ALIGNED, None) == sk.ERR_ALIGNMENT
     assert lib.skinny_tile_workspace_bytes(None) == sk.ERR_INVALID_ARG
     assert lib.skinny_tile_device_error(0, None) == sk.ERR_INVALID_ARG
 
