@@ -4,17 +4,17 @@ or FP8 E4M3 (+ FP32 per output channel), FP16 activations, FP32 accumulation;
 products for any number of tokens, grouped by expert (the same formats) or in
 8-bit integers; and the verification of drafted tokens.
 
-This module is a thin ctypes binding over ``libskinny.so`` (whose C ABI is
+This module is a thin binding over ``libskinny.so`` (whose C ABI is
 ``include/skinny.h``): it turns numpy arrays and torch tensors into pointers,
-sizes and a stream handle, calls the library, and raises ``SkinnyError`` on a
-non-zero status.  Every step of the GEMM runs in the library's CUDA kernels;
+sizes and a stream handle, calls the library (by ctypes, or from ``_binding.so``
+where a call is short), and raises ``SkinnyError`` on a non-zero status.  Every
+step of the GEMM runs in the library's CUDA kernels;
 there is no fallback: if the library is missing, the first call raises.
 """
 from __future__ import annotations
 
 import ctypes
 import dataclasses
-import functools
 import os
 import threading
 
@@ -454,55 +454,35 @@ def device_error(clear: bool = True) -> int:
 # Products for any number of tokens: experts and 8-bit integers
 # ---------------------------------------------------------------------------
 
-def _device_of(x, *others) -> int:
-    """The index of x's CUDA device, which every other tensor must be on."""
-    d = x.get_device()
-    for t in others:
-        if t is not None and t.get_device() != d:
-            raise ValueError("tensors on one device expected: %s and %s" % (x.device, t.device))
-    if d < 0:
-        raise ValueError("tensors on a CUDA device expected, got %s" % x.device)
-    return d
+_native = None
 
 
-def _launch(name, d, stream, *args) -> None:
-    """Calls the library's `name` with the stream as its last argument, with device d current."""
-    import torch
+def binding():
+    """The compiled binding of the calls below (``_binding.so``, built by
+    ``__graft_entry__.build()``), given the loaded library's functions; raise if absent."""
+    global _native
+    if _native is None:
+        import importlib.util
 
-    fn = getattr(_lib or library(), name)
-    if d == torch._C._cuda_getDevice():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream)
-    else:
-        with torch.cuda.device(d):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream)
-    if st != OK:
-        raise SkinnyError(st, name)
+        import torch  # noqa: F401  (its libraries are loaded first)
+
+        path = os.path.join(_PKG, "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError("_binding.so is not built (%s); run __graft_entry__.build()" % path)
+        spec = importlib.util.spec_from_file_location(__name__ + "._binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        lib = library()
+        module.bind(SkinnyError, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "skinny_gemm_experts", "skinny_gemm_experts_silu_mul", "skinny_quantize_int8", "skinny_int8_gemm",
+            "skinny_verify_draft")))
+        _native = module
+    return _native
 
 
 def _given(*outputs):
     if any(t is None for t in outputs):
         raise ValueError("the output tensors must be given")
-
-
-def _ws(workspace):
-    if workspace is None:
-        return None, 0
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def _output(y, x, rows, cols, out_dtype):
-    """(y, its SKINNY_OUT code); y None: a new tensor on x's device."""
-    import torch
-
-    if y is None:
-        y = x.new_empty((rows, cols), dtype=out_dtype or torch.float16)
-    elif y.shape != (rows, cols) or not y.is_contiguous():
-        raise ValueError("y must be a contiguous float16/float32 [%d, %d] tensor" % (rows, cols))
-    if y.dtype == torch.float16:
-        return y, OUT_F16
-    if y.dtype == torch.float32:
-        return y, OUT_F32
-    raise ValueError("y must be a contiguous float16/float32 [%d, %d] tensor" % (rows, cols))
 
 
 def tile_workspace_bytes() -> int:
@@ -532,10 +512,11 @@ def _pack_experts(fmt, codes, scales, E, N, K, gate_up):
     nb = int(library().skinny_experts_packed_bytes(fmt, E, N, K, int(gate_up)))
     if nb == 0:
         raise SkinnyError(ERR_INVALID_ARG, "pack_experts shape")
-    d = _device_of(codes, scales)
     out = torch.empty(nb, dtype=torch.uint8, device=codes.device)
-    _launch("skinny_pack_experts", d, None, fmt, codes.data_ptr(), scales.data_ptr() if scales is not None else None,
-            E, N, K, int(gate_up), out.data_ptr())
+    with torch.cuda.device(codes.device):
+        st = library().skinny_pack_experts(fmt, codes.data_ptr(), scales.data_ptr() if scales is not None else None,
+                                           E, N, K, int(gate_up), out.data_ptr(), _stream_handle(None))
+    _check(st, "skinny_pack_experts")
     return out
 
 
@@ -613,21 +594,10 @@ class PackedExpertsFP8:
 
 def _gemm_experts(y, x, w, offsets, out_dtype, workspace, stream, silu):
     """The experts' product into y, or into a new tensor of out_dtype; returns it."""
-    import torch
-
     if w.gate_up != silu:
         raise TypeError("gemm_experts takes experts packed without gate_up, gemm_experts_silu_mul with it")
-    if x.dtype != torch.float16 or x.dim() != 2 or x.shape[1] != w.K or not x.is_contiguous():
-        raise ValueError("x must be a contiguous float16 [T, %d] tensor" % w.K)
-    if offsets.dtype != torch.int32 or offsets.shape != (w.E + 1,) or not offsets.is_contiguous():
-        raise ValueError("offsets must be a contiguous int32 [%d] tensor" % (w.E + 1))
-    T, outputs = x.shape[0], w.N // 2 if silu else w.N
-    y, out = _output(y, x, T, outputs, out_dtype)
-    ws_ptr, ws_bytes = _ws(workspace)
-    d = _device_of(x, y, w.data, w.scale, offsets, workspace)
-    _launch("skinny_gemm_experts_silu_mul" if silu else "skinny_gemm_experts", d, stream, w.fmt, x.data_ptr(), T, w.K,
-            offsets.data_ptr(), w.E, w.data.data_ptr(), w.scale.data_ptr(), outputs, y.data_ptr(), out, ws_ptr, ws_bytes)
-    return y
+    return (_native or binding()).gemm_experts(silu, y, x, w.fmt, w.E, w.N, w.K, w.data, w.scale, offsets, out_dtype,
+                                               workspace, stream)
 
 
 def gemm_experts_into(y, x, w, offsets, workspace=None, stream=None) -> None:
@@ -681,72 +651,28 @@ class WeightInt8:
         return int(self.codes.shape[1])
 
 
-def _quantize_int8(q, row_scale, x, stream):
-    import torch
-
-    if x.dtype == torch.float16:
-        kind = OUT_F16
-    elif x.dtype == torch.float32:
-        kind = OUT_F32
-    else:
-        kind = None
-    if kind is None or x.dim() != 2 or not x.is_contiguous():
-        raise ValueError("x must be a contiguous float16/float32 [M, K] tensor")
-    M, K = x.shape
-    if q is None:
-        q = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
-        row_scale = x.new_empty(M, dtype=torch.float32)
-    elif q.shape != x.shape or q.dtype != torch.int8 or not q.is_contiguous():
-        raise ValueError("q must be a contiguous int8 tensor of x's shape")
-    elif row_scale.shape != (M,) or row_scale.dtype != torch.float32 or not row_scale.is_contiguous():
-        raise ValueError("row_scale must be a contiguous float32 [M] tensor")
-    _launch("skinny_quantize_int8", _device_of(x, q, row_scale), stream, x.data_ptr(), kind, M, K, q.data_ptr(),
-            row_scale.data_ptr())
-    return q, row_scale
-
-
 def quantize_int8_into(q, row_scale, x, stream=None) -> None:
     """Rows of x (float16 or float32 [M, K]) to 8-bit integers: row_scale =
     max|x| / 127, q = round(x / row_scale).  q int8 [M, K], row_scale float32 [M]."""
     _given(q, row_scale)
-    _quantize_int8(q, row_scale, x, stream)
+    (_native or binding()).quantize_int8(q, row_scale, x, stream)
 
 
 def quantize_int8(x, stream=None):
     """Allocate and return (q int8 [M, K], row_scale float32 [M]): see quantize_int8_into."""
-    return _quantize_int8(None, None, x, stream)
-
-
-def _gemm_int8(y, q, row_scale, w, out_dtype, workspace, stream):
-    import torch
-
-    codes, channel_scale = w.codes, w.channel_scale
-    N, K = codes.shape
-    if q.dtype != torch.int8 or q.dim() != 2 or not q.is_contiguous():
-        raise ValueError("q must be a contiguous int8 [M, %d] tensor" % K)
-    M, k = q.shape
-    if k != K:
-        raise ValueError("q must be a contiguous int8 [M, %d] tensor" % K)
-    if row_scale.dtype != torch.float32 or row_scale.shape != (M,) or not row_scale.is_contiguous():
-        raise ValueError("row_scale must be a contiguous float32 [M] tensor")
-    y, out = _output(y, q, M, N, out_dtype)
-    ws_ptr, ws_bytes = _ws(workspace)
-    _launch("skinny_int8_gemm", _device_of(q, y, row_scale, codes, channel_scale, workspace), stream, q.data_ptr(),
-            row_scale.data_ptr(), M, K, codes.data_ptr(), channel_scale.data_ptr(), N, y.data_ptr(), out, ws_ptr,
-            ws_bytes)
-    return y
+    return (_native or binding()).quantize_int8(None, None, x, stream)
 
 
 def gemm_int8_into(y, q, row_scale, w: "WeightInt8", workspace=None, stream=None) -> None:
     """y[m, n] = (q[m] . w[n]) * row_scale[m] * channel_scale[n], the sum exact
     (y float16 or float32, preallocated; any number of rows)."""
     _given(y)
-    _gemm_int8(y, q, row_scale, w, None, workspace, stream)
+    (_native or binding()).gemm_int8(y, q, row_scale, w.codes, w.channel_scale, None, workspace, stream)
 
 
 def gemm_int8(q, row_scale, w: "WeightInt8", out_dtype=None, workspace=None, stream=None):
     """Allocate y [M, N] (float16 unless out_dtype says otherwise): see gemm_int8_into."""
-    return _gemm_int8(None, q, row_scale, w, out_dtype, workspace, stream)
+    return (_native or binding()).gemm_int8(None, q, row_scale, w.codes, w.channel_scale, out_dtype, workspace, stream)
 
 
 def tile_device_error(clear: bool = True) -> int:
@@ -759,55 +685,6 @@ def tile_device_error(clear: bool = True) -> int:
 # ---------------------------------------------------------------------------
 # Verification of drafted tokens
 # ---------------------------------------------------------------------------
-
-@functools.lru_cache(maxsize=None)
-def _prob_dtypes():
-    import torch
-
-    return {torch.float16: PROB_F16, torch.float32: PROB_F32, torch.bfloat16: PROB_BF16}
-
-
-def _verify_draft(tokens, accepted, target, draft, draft_tokens, uniform, num_drafts, stream):
-    import torch
-
-    kind = _prob_dtypes().get(target.dtype)
-    if kind is None or target.dim() != 3:
-        raise ValueError("target must be a float32/float16/bfloat16 [B, S+1, V] tensor")
-    B, S, V = target.shape
-    S -= 1
-    if S < 0 or V < 1:
-        raise ValueError("target must be a float32/float16/bfloat16 [B, S+1, V] tensor")
-    target_b, target_s, one = target.stride()
-    if V > 1 and one != 1:
-        raise ValueError("target must have unit stride along V")
-    draft_ptr, draft_b, draft_s = None, 0, 0
-    if draft is not None:
-        if draft.dtype != target.dtype or draft.shape != (B, S, V):
-            raise ValueError("draft must be a [%d, %d, %d] tensor of target's dtype" % (B, S, V))
-        draft_b, draft_s, one = draft.stride()
-        if V > 1 and one != 1:
-            raise ValueError("draft must have unit stride along V")
-        draft_ptr = draft.data_ptr() if S > 0 else None
-    i32, shape = torch.int32, (B, S + 1)
-    if draft_tokens.dtype != i32 or draft_tokens.shape != (B, S) or not draft_tokens.is_contiguous():
-        raise ValueError("draft_tokens must be a contiguous int32 [%d, %d] tensor" % (B, S))
-    if uniform.dtype != torch.float32 or uniform.shape != shape or not uniform.is_contiguous():
-        raise ValueError("uniform must be a contiguous float32 [%d, %d] tensor" % shape)
-    if num_drafts is not None and (num_drafts.dtype != i32 or num_drafts.shape != (B,) or not num_drafts.is_contiguous()):
-        raise ValueError("num_drafts must be a contiguous int32 [%d] tensor" % B)
-    if tokens is None:
-        tokens = torch.empty_like(uniform, dtype=i32)
-        accepted = tokens.new_empty(B)
-    elif tokens.dtype != i32 or tokens.shape != shape or not tokens.is_contiguous():
-        raise ValueError("tokens must be a contiguous int32 [%d, %d] tensor" % shape)
-    elif accepted.dtype != i32 or accepted.shape != (B,) or not accepted.is_contiguous():
-        raise ValueError("accepted must be a contiguous int32 [%d] tensor" % B)
-    d = _device_of(target, draft, draft_tokens, uniform, num_drafts, tokens, accepted)
-    _launch("skinny_verify_draft", d, stream, target.data_ptr(), target_b, target_s, draft_ptr, draft_b, draft_s, kind,
-            draft_tokens.data_ptr() if S else None, uniform.data_ptr(),
-            num_drafts.data_ptr() if num_drafts is not None else None, B, S, V, tokens.data_ptr(), accepted.data_ptr())
-    return tokens, accepted
-
 
 def verify_draft_into(tokens, accepted, target, draft, draft_tokens, uniform, num_drafts=None, stream=None) -> None:
     """A verify round against the target's probabilities, from given random
@@ -823,9 +700,9 @@ def verify_draft_into(tokens, accepted, target, draft, draft_tokens, uniform, nu
     accepted      int32 [B]
     """
     _given(tokens, accepted)
-    _verify_draft(tokens, accepted, target, draft, draft_tokens, uniform, num_drafts, stream)
+    (_native or binding()).verify_draft(tokens, accepted, target, draft, draft_tokens, uniform, num_drafts, stream)
 
 
 def verify_draft(target, draft, draft_tokens, uniform, num_drafts=None, stream=None):
     """Allocate and return (tokens int32 [B, S+1], accepted int32 [B]): see verify_draft_into."""
-    return _verify_draft(None, None, target, draft, draft_tokens, uniform, num_drafts, stream)
+    return (_native or binding()).verify_draft(None, None, target, draft, draft_tokens, uniform, num_drafts, stream)

@@ -1,4 +1,5 @@
-"""Build libskinny.so in-tree with nvcc for sm_100a.
+"""Build libskinny.so in-tree with nvcc for sm_100a, and the Python binding of
+the calls for any number of tokens (_binding.so) with g++.
 
     python -m fp8_weight_only_w4a16_b200.build [--verbose]
 """
@@ -17,6 +18,8 @@ SOURCES = [os.path.join(CSRC, f) for f in ("skinny.cu", "stream_read.cu", "tile_
 HEADERS = [os.path.join(CSRC, "layout.h"), os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "tcgen05.cuh"),
            os.path.join(ROOT, "include", "skinny.h")]
 LIBRARY = os.path.join(PKG, "libskinny.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -51,6 +54,32 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIBRARY
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile _binding.so against the installed torch (its headers and libraries)."""
+    import sysconfig
+
+    import torch
+
+    newest = max(os.path.getmtime(f) for f in (BINDING_SOURCE, os.path.join(ROOT, "include", "skinny.h")))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
+    for d in (os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+              sysconfig.get_paths()["include"], os.path.join(cuda, "include")):
+        cmd += ["-I", d]
+    cmd += [BINDING_SOURCE, "-o", tmp, "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed:\n%s\n%s" % (" ".join(cmd), r.stderr))
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 if __name__ == "__main__":
     build(force=True, verbose="--verbose" in sys.argv)
+    build_binding(force=True)
     print(LIBRARY)
