@@ -43,6 +43,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "../../include/skinny.h"
@@ -187,15 +188,36 @@ __device__ __forceinline__ int find(const int* a, int n, int v)
     return lo;
 }
 
+// What a tile of TN columns takes, in ns, as measured with many tiles: a block,
+// the epilogue, and the exchange of partial sums where tiles are split.
+struct TileCost {
+    int block, epilogue, exchange;
+};
+
+__host__ __device__ constexpr TileCost tile_cost(int TN)
+{
+    return TN <= 16   ? TileCost{270, 1500, 1500}
+           : TN <= 32 ? TileCost{270, 2000, 2000}
+           : TN <= 64 ? TileCost{270, 3500, 5000}
+           : TN <= 128 ? TileCost{320, 5000, 10000}
+                       : TileCost{420, 6500, 20000};
+}
+
 // Which tiles are split, and how their blocks are shared out (see Walk).
-template <bool PAIR>
+template <int TN, bool PAIR>
 __device__ __forceinline__ void finish_schedule(Schedule& s, const Params& p, int total)
 {
     const int P = PAIR ? gridDim.x / 2 : gridDim.x;
     int splits = 0;
     if (p.partials != nullptr) {
+        // The last round's `rest` tiles take C blocks' time if they are not
+        // split, and rest * C / P and the exchange if they are.  A product of
+        // 2048 x 5120 with 34816 channels takes 305 us with its rest whole and
+        // 356 split, 2048 x 1024 with 1024 channels 16.6 and 27.4.
         const int rest = total % P;
-        splits = rest == 0 || 4 * rest >= P || total < P ? rest : rest + P;
+        constexpr TileCost cost = tile_cost(TN);
+        if (rest != 0 && (int64_t)p.C * (P - rest) * cost.block > (int64_t)cost.exchange * P)
+            splits = 4 * rest >= P || total < P ? rest : rest + P;
     }
     s.total = total;
     s.splits = splits;
@@ -428,7 +450,7 @@ __device__ void make_schedule(Schedule& s, const Params& p)
         s.rows[0] = first;
         s.tiles[0] = 0;
     }
-    if (lane == 31) finish_schedule<PAIR>(s, p, run);
+    if (lane == 31) finish_schedule<TN, PAIR>(s, p, run);
     __syncwarp();
 }
 
@@ -638,7 +660,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             s.rows[1] = p.T;
             s.tiles[0] = 0;
             s.tiles[1] = token_tiles(p.T, TN) * row_groups<C::kPair>(p);
-            finish_schedule<C::kPair>(s, p, s.tiles[1]);
+            finish_schedule<TN, C::kPair>(s, p, s.tiles[1]);
         }
     } else {
         ptx::pdl_wait_prior_grid();
@@ -1150,6 +1172,22 @@ int launch(Params p, const void* x, const void* w, int grid, cudaStream_t stream
     return cudaLaunchKernelEx(&cfg, tile_gemm<FMT, TN, SILU>, p, xm, xm2, wm, wm2) == cudaSuccess ? SKINNY_OK : SKINNY_ERR_CUDA;
 }
 
+// The time of a launch with tiles of TN tokens by tile_cost: in whole rounds
+// or with its last round split, whichever the kernel will take.
+int64_t launch_time(const Params& p, int TN, int grid)
+{
+    const TileCost cost = tile_cost(TN);
+    const int64_t pair = TN > 64 ? 2 : 1, P = std::max<int64_t>(grid / pair, 1);
+    // an expert's last tile is half full on average
+    const int64_t columns = p.E == 1 ? ((int64_t)p.T + TN - 1) / TN
+                                     : std::max<int64_t>(std::min(p.E, p.T), p.T / TN + p.E / 2);
+    const int64_t tiles = columns * ((p.G + pair - 1) / pair);
+    const int64_t tile = std::max<int64_t>((int64_t)p.C * cost.block, cost.epilogue);
+    const int64_t whole = (tiles + P - 1) / P * tile + cost.epilogue;
+    if (p.partials == nullptr) return whole;
+    return std::min(whole, tiles * tile / P + cost.epilogue + cost.exchange);
+}
+
 // Token columns per tile: `rows` is the number a tile would like to hold.
 // Narrow tiles leave the shared memory to the weights' ring (the memory-bound
 // range); wide ones reuse each decoded block more often.
@@ -1159,8 +1197,18 @@ int launch_any(const Params& p, const void* x, const void* w, int64_t rows, int 
     if (rows <= 16) return launch<FMT, 16, SILU>(p, x, w, grid, stream);
     if (rows <= 32) return launch<FMT, 32, SILU>(p, x, w, grid, stream);
     if (rows <= 64) return launch<FMT, 64, SILU>(p, x, w, grid, stream);
-    if (rows <= 128) return launch<FMT, 128, SILU>(p, x, w, grid, stream);
-    return launch<FMT, kWidest<FMT>, SILU>(p, x, w, grid, stream);
+    // More tokens: a wide tile reads the weights fewer times, a narrower one
+    // leaves fewer SMs idle where wide tiles are few.  Of those that do not
+    // exceed the tokens, the one with the least time by tile_cost: 200 x 4096
+    // with 6000 channels takes 15.8 us with 128 and 18.9 with 256, 2048 x 5120
+    // with 34816 channels 460 with 128 and 305 with 256.
+    constexpr int kWide = kWidest<FMT>;
+    const int64_t t64 = launch_time(p, 64, grid);
+    const int64_t t128 = launch_time(p, 128, grid);
+    const int64_t wide = rows <= 128 ? INT64_MAX : launch_time(p, kWide, grid);
+    if (wide <= t64 && wide <= t128) return launch<FMT, kWide, SILU>(p, x, w, grid, stream);
+    if (t128 <= t64) return launch<FMT, 128, SILU>(p, x, w, grid, stream);
+    return launch<FMT, 64, SILU>(p, x, w, grid, stream);
 }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }

@@ -97,6 +97,29 @@ def test_store(fmt, N, K, counts, out, split):
         assert not ws[-32 * torch.cuda.get_device_properties(0).multi_processor_count:].any()
 
 
+@pytest.mark.parametrize("fmt,N,K,counts", [
+    ("nvfp4", 260, 5120, [20]),
+    ("fp8", 300, 5120, [20, 0, 25]),
+    ("nvfp4", 1000, 5120, [33, 64, 1]),
+    ("nvfp4", 19200, 5120, [100]),
+    ("fp8", 6400, 16384, [570]),
+])
+def test_split_tiles_of_every_width(fmt, N, K, counts):
+    """Products whose last tiles are split along K (with 148 SMs), from 32 to 192 tokens wide;
+    of many tokens every thirteenth is looked at."""
+    off = offsets_of(counts)
+    logical, w, x = make(fmt, len(counts), N, K, int(off[-1]))
+    seen = np.arange(0, len(x), 13 if len(x) > 99 else 1)
+    seen_off = np.searchsorted(seen, off).astype(np.int32)
+    ref, bound = expected(fmt, logical, x[seen], seen_off)
+    for ws in (sk.make_experts_workspace(), None):
+        y = sk.gemm_experts(dev(x), w, dev(off), torch.float32, workspace=ws)
+        done()
+        assert_parity(y.double().cpu().numpy()[seen], ref, bound, "f32", "%s %dx%d %s" % (fmt, N, K, counts))
+        if ws is not None:
+            assert not ws[-32 * torch.cuda.get_device_properties(0).multi_processor_count:].any()
+
+
 @pytest.mark.parametrize("out", ["f32", "f16"])
 @pytest.mark.parametrize("fmt,F,K,counts", [
     ("nvfp4", 64, 512, [1]),

@@ -80,6 +80,24 @@ def test_product(M, N, K, out, split):
     assert np.array_equal(y.cpu().numpy(), product(q, rs, c, cs, out))
 
 
+@pytest.mark.parametrize("M,N,K", [(20, 300, 5120), (61, 300, 5120), (61, 19000, 5120), (100, 19200, 5120),
+                                   (300, 6400, 16384), (1020, 5120, 16384)])
+def test_split_tiles_of_every_width(M, N, K):
+    """Products whose last tiles are split along K (with 148 SMs), from 32 to 256 tokens wide."""
+    rng = np.random.default_rng(M + N + K)
+    q, c = rng.integers(-128, 128, (M, K), dtype=np.int8), rng.integers(-128, 128, (N, K), dtype=np.int8)
+    rs, cs = (rng.uniform(0.5, 1.5, n).astype(np.float32) / 1000 for n in (M, N))
+    d = lambda a: torch.from_numpy(a).to(DEV)
+    w, dq, drs = sk.WeightInt8(d(c), d(cs)), d(q), d(rs)
+    acc = dq.double() @ d(c).double().T                            # exact: below 2^53
+    expected = acc.float() * drs[:, None] * d(cs)[None]
+    for ws in (sk.make_int8_workspace(), None):
+        assert torch.equal(sk.gemm_int8(dq, drs, w, torch.float32, workspace=ws), expected)
+        if ws is not None:                                         # the flags are free again
+            assert not ws[-32 * torch.cuda.get_device_properties(0).multi_processor_count:].any()
+    done()
+
+
 def test_largest_sums_do_not_wrap():
     K = 131056
     q = np.full((2, K), -128, np.int8)
