@@ -230,6 +230,38 @@ __device__ __forceinline__ unsigned ld_acquire_gpu(const unsigned* p)
     return v;
 }
 
+// Loads and stores under a predicate.  The compiler makes a branch of a
+// condition around a store, ~40 clocks each where the stores are unrolled.
+__device__ __forceinline__ uint32_t ld_global_cg_if(const unsigned* p, bool on)
+{
+    uint32_t v;
+    asm volatile("{\n\t.reg .pred on;\n\tsetp.ne.b32 on, %2, 0;\n\tmov.b32 %0, 0;\n\t"
+                 "@on ld.global.cg.u32 %0, [%1];\n\t}"
+                 : "=&r"(v)
+                 : "l"(p), "r"((int)on)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_global_if(unsigned* p, uint32_t v, bool on)
+{
+    asm volatile("{\n\t.reg .pred on;\n\tsetp.ne.b32 on, %2, 0;\n\t@on st.global.b32 [%0], %1;\n\t}" ::"l"(p), "r"(v),
+                 "r"((int)on)
+                 : "memory");
+}
+
+__device__ __forceinline__ void st_global_if(float* p, float v, bool on)
+{
+    st_global_if(reinterpret_cast<unsigned*>(p), __float_as_uint(v), on);
+}
+
+__device__ __forceinline__ void st_global_if(__half* p, __half v, bool on)
+{
+    asm volatile("{\n\t.reg .pred on;\n\tsetp.ne.b32 on, %2, 0;\n\t@on st.global.b16 [%0], %1;\n\t}" ::"l"(p),
+                 "h"(__half_as_ushort(v)), "r"((int)on)
+                 : "memory");
+}
+
 // A warp's 32 lanes of tensor memory, n consecutive 32-bit columns per lane.
 // A load waits for its own completion inside the one statement, so no use of
 // the registers can be moved before the wait.

@@ -188,8 +188,9 @@ __device__ __forceinline__ int find(const int* a, int n, int v)
     return lo;
 }
 
-// What a tile of TN columns takes, in ns, as measured with many tiles: a block,
-// the epilogue, and the exchange of partial sums where tiles are split.
+// What a tile of TN columns takes, in ns: a block, the epilogue (what is left
+// of a tile without blocks), and the exchange of partial sums where tiles are
+// split.  Fitted to 27 shapes of both kinds, each run at every width.
 struct TileCost {
     int block, epilogue, exchange;
 };
@@ -198,7 +199,7 @@ __host__ __device__ constexpr TileCost tile_cost(int TN)
 {
     return TN <= 16   ? TileCost{270, 1500, 1500}
            : TN <= 32 ? TileCost{270, 2000, 2000}
-           : TN <= 64 ? TileCost{270, 3500, 5000}
+           : TN <= 64 ? TileCost{270, 3500, 3000}
            : TN <= 128 ? TileCost{320, 5000, 10000}
                        : TileCost{420, 6500, 20000};
 }
@@ -454,20 +455,20 @@ __device__ void make_schedule(Schedule& s, const Params& p)
     __syncwarp();
 }
 
-// Stores r[0..n) at y[at], y[at + step], ...
+// Stores r[0..n) at y[at], y[at + step], ...  A branch around each store made
+// a tile of 192 columns 10000 clocks, longer than 20 blocks of it: 8192 rows, 4
+// experts of 2048 x 256 took 34.8 us for 20.1 with predicates.
 template <int N>
 __device__ __forceinline__ void put_column(void* y, int64_t at, int step, const float (&r)[N], int n, int f32)
 {
     if (f32) {
         float* p = static_cast<float*>(y) + at;
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (j < n) p[(int64_t)j * step] = r[j];
+        for (int j = 0; j < N; ++j, p += step) ptx::st_global_if(p, r[j], j < n);
     } else {
         __half* p = static_cast<__half*>(y) + at;
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (j < n) p[(int64_t)j * step] = __float2half_rn(r[j]);
+        for (int j = 0; j < N; ++j, p += step) ptx::st_global_if(p, __float2half_rn(r[j]), j < n);
     }
 }
 
@@ -529,7 +530,7 @@ __device__ __forceinline__ void add_partials(const Params& p, const Walk<TN, PAI
                 const bool there = c - i >= lowest && !walk.empty(c - i);
                 const unsigned* slot = p.partials + (int64_t)walk.slot(c - i) * kSlotWords + row + c0 * kRows;
 #pragma unroll
-                for (int j = 0; j < COLS; ++j) part[i][j] = there && j < left ? __ldcg(slot + j * kRows) : 0;
+                for (int j = 0; j < COLS; ++j) part[i][j] = ptx::ld_global_cg_if(slot + j * kRows, there && j < left);
             }
 #pragma unroll
             for (int i = 0; i < SLOTS; ++i)
@@ -676,9 +677,11 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
     Producer<FMT, TN> producer;
     if (!C::kInt8 && warp == 0 && ptx::elect_one()) {
         // the warp that made the schedule starts on its ring before the CTA is
-        // ready: with two slots, as a copy takes ~160 ns to issue
+        // ready: with two slots, as a copy takes ~160 ns to issue.  The other
+        // CTA of a pair would wait for them: 62.5 us for 58.5 (8192 rows, 64
+        // experts of 2048 x 1024).
         producer.begin(s, p);
-        producer.produce(sm, r, issued, 2, s, p, &w_map, &w_map2, leader);
+        if (!C::kPair) producer.produce(sm, r, issued, 2, s, p, &w_map, &w_map2, leader);
     }
     __syncwarp();
     ptx::tc_fence_before();
@@ -882,7 +885,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             // rows and their 16 up rows in the two halves of every warp.
             const int o = SILU ? g.row_tile * 64 + q * 16 + (lane & 15) : g.row_tile * kRows + row;
             const bool valid = o < p.outputs;
-            float scale = 0.f, rs = 0.f;      // loaded while the tile is computed
+            float scale = 0.f;      // loaded while the tile is computed
             if (valid && !publish) {
                 if (FMT == SKINNY_FMT_NVFP4) scale = p.scale[g.e];
                 else if (FMT == SKINNY_FMT_FP8)
@@ -894,7 +897,16 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             constexpr int kCols = TN <= 16 ? 8 : TN <= 64 ? 16 : 32;
             constexpr int kNext = kCols * kTurns;
             const int c_first = turn * kCols;
-            if (C::kInt8 && !publish && c_first + lane < g.n) rs = p.row_scale[g.t0 + c_first + lane];
+            // the row scales of all its chunks, of each chunk's column `lane`
+            constexpr int kMine = TN / kNext;
+            float rs[kMine] = {};
+            if (C::kInt8 && !publish) {
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    const int c = c_first + i * kNext + lane;
+                    if (c < g.n) rs[i] = p.row_scale[g.t0 + c];
+                }
+            }
             ok = wait_warp(sm.d_full(dr.i), dr.phase, &s.abort, kErrAccumulator);
             if (!ok) break;
             ptx::tc_fence_after();
@@ -931,17 +943,13 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             }
 #pragma unroll 1
             for (int c0 = c_first; c0 < g.n; c0 += kNext) {
-                // the next chunk's row scales, ahead of this one's stores
-                float rs_next = 0.f;
-                if (C::kInt8 && !publish && c0 + kNext + lane < g.n) rs_next = p.row_scale[g.t0 + c0 + kNext + lane];
                 uint32_t v[kCols];
                 ptx::tmem_ld(acc + c0, v);
                 const int left = g.n - c0;
                 if (publish) {
                     unsigned* slot = p.partials + (size_t)blockIdx.x * kSlotWords + row + c0 * kRows;
 #pragma unroll
-                    for (int j = 0; j < kCols; ++j)
-                        if (j < left) slot[j * kRows] = v[j];
+                    for (int j = 0; j < kCols; ++j) ptx::st_global_if(slot + j * kRows, v[j], j < left);
                     continue;
                 }
                 // y of this thread's channel at the chunk's first token
@@ -962,12 +970,13 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                     float r[kCols];
 #pragma unroll
                     for (int j = 0; j < kCols; ++j) {
-                        if constexpr (C::kInt8) r[j] = (float)(int)v[j] * __shfl_sync(~0u, rs, j) * scale;
+                        if constexpr (C::kInt8) r[j] = (float)(int)v[j] * __shfl_sync(~0u, rs[0], j) * scale;
                         else r[j] = __uint_as_float(v[j]) * scale;
                     }
                     put_column<kCols>(p.y, at, p.outputs, r, valid ? left : 0, p.out_f32);
                 }
-                rs = rs_next;
+#pragma unroll
+                for (int i = 1; i < kMine; ++i) rs[i - 1] = rs[i];
             }
             ptx::tc_fence_before();
             __syncwarp();
