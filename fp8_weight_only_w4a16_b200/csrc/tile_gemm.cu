@@ -35,9 +35,12 @@
 //                     65 us (5.4 TB/s); a block takes its two groups ~430
 //                     clocks, HBM ~390.
 //   many rows         the tensor cores under the power limit: 16387 rows over
-//                     32 experts of 2816 x 5120, 358 to 385 us (1.23 to 1.32
-//                     PFLOP/s); int8 2048 x 34816 x 5120, 290 to 330 us (2.2
+//                     32 experts of 2816 x 5120, 346 to 390 us (1.21 to 1.37
+//                     PFLOP/s); int8 2048 x 34816 x 5120, 290 to 318 us (2.3
 //                     to 2.5 POP/s, at 1.1 to 1.3 GHz).
+//   hundreds of rows  launch, first loads and an epilogue, 6 to 8 us together, and
+//                     the last round's idle SMs: 1003 rows over 32 experts of
+//                     2051 x 2048, 26 us; int8 200 x 6000 x 4096, 15 us.
 //   one token         latency: eight experts of 2816 x 2048 (23 MB) 13 us.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -130,7 +133,9 @@ struct Cfg {
     static constexpr int kGroups = kInt8 ? 0 : 2;
     static constexpr int kACol = 512 - 64 * kStepBlocks * kGroups;
     static constexpr int kDecodeWarps = 4 * kGroups;
-    // int8's wide tiles are computed in less time than four warps store them.
+    // int8's wide tiles of few blocks are computed in less time than four warps
+    // store them: 700 x 2048 with 12000 channels takes 24.1 us with eight, 25.5
+    // with four; from 40 blocks on there is no difference.
     static constexpr int kEpilogueWarps = kInt8 && kPair ? 8 : 4;
     static constexpr int kWarps = 4 + kDecodeWarps + kEpilogueWarps;
     static constexpr int kThreads = kWarps * 32;
