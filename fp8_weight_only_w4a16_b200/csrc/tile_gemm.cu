@@ -100,6 +100,18 @@ struct Params {
 
 constexpr int at_most(int a, int b) { return a < b ? a : b; }
 
+// Tiles of more columns than this are computed by pairs of CTAs.
+__host__ __device__ constexpr bool is_pair(int TN) { return TN > 64; }
+
+// Columns that the matrix instruction of a tile with n tokens has: it takes
+// multiples of 16, a pair's of 32.  Columns past n hold other tokens' rows, or
+// zeros, and are not stored.
+__host__ __device__ constexpr int columns(int n, bool pair)
+{
+    const int step = pair ? 32 : 16;
+    return (n + step - 1) / step * step;
+}
+
 // A step is what one turn of every role handles: two K blocks of a narrow
 // tile, one of a wide one.  Every turn of a decoder or of the MMA thread costs
 // it some hundred clocks of waits, arrivals and commits beside its work, and a
@@ -113,7 +125,7 @@ struct Cfg {
     // in each CTA, and half the tokens' rows loaded by each.  One CTA by itself
     // would read 96 bytes (experts: 80) from L2 per clock of matrix instructions,
     // where an SM gets about 64.
-    static constexpr bool kPair = TN > 64;
+    static constexpr bool kPair = is_pair(TN);
     static constexpr int kStepBlocks = kPair ? 1 : 2;
     static constexpr int kTokens = kPair ? TN / 2 : TN;                         // tokens in this CTA's slots
     static constexpr int kChunksPerBlock = kInt8 ? 1 : 2;                       // 128-byte wide pieces of x per block
@@ -157,11 +169,12 @@ struct Cfg {
     static_assert(kChunkBytes % 1024 == 0 && kWBytes % 1024 == 0 && kBox * 128 % 1024 == 0,
                   "swizzled tiles start on 1024 bytes");
     static_assert(kXStages >= 3 && kWStages >= 3, "rings");
+    static_assert(columns(TN, kPair) == TN, "a full tile has no columns to spare");
 };
 
 // The tile sequence, from the experts' row counts: expert e has
-// ceil(rows / TN) token tiles of q_e rows each (a multiple of 16, so the
-// tiles of one expert are alike) times G row tiles.
+// ceil(rows / TN) token tiles of q_e rows each (a whole number of the matrix
+// instruction's steps, so the tiles of one expert are alike) times G row tiles.
 struct Schedule {
     int tiles[kMaxExperts + 1];          // running number of tiles
     int rows[kMaxExperts + 1];           // running row offset (offsets made monotone and clamped to [0, T])
@@ -172,7 +185,6 @@ struct Schedule {
 };
 
 __device__ __forceinline__ int token_tiles(int rows, int TN) { return (rows + TN - 1) / TN; }
-__device__ __forceinline__ int tile_rows(int rows, int nt) { return ((rows + nt - 1) / nt + 15) & ~15; }
 
 // What a tile has of the weight's row tiles: one, or a pair's two.
 template <bool PAIR>
@@ -294,7 +306,11 @@ struct Walk {
         }
         g.e = find(s.tiles, p.E, g.tile);
         const int m = s.rows[g.e + 1] - s.rows[g.e];
-        const int q = m <= TN ? (m + 15) & ~15 : tile_rows(m, token_tiles(m, TN));
+        int q = m;
+        if (m > TN) {
+            const int nt = token_tiles(m, TN);
+            q = columns((m + nt - 1) / nt, PAIR);
+        }
         const int lt = g.tile - s.tiles[g.e];
         const int groups = row_groups<PAIR>(p), tt = quotient(lt, groups, p.rcp_groups), rt = lt - tt * groups;
         g.row_tile = PAIR ? rt * 2 + (int)(blockIdx.x & 1) : rt;
@@ -587,7 +603,7 @@ struct Producer {
                 // (an odd last row tile has no partner: its pair's second CTA computes it too, and stores nothing)
                 rt = C::kPair && g.row_tile >= p.G ? p.G - 1 : g.row_tile;
                 src = C::kInt8 ? nullptr : p.w + ((size_t)g.e * p.G + rt) * p.C * block_bytes(FMT);
-                pair_bytes = 2 * (C::kWBytes + (((g.n + 15) & ~15) / 2 + C::kBox - 1) / C::kBox * C::kBox * 128);
+                pair_bytes = 2 * (C::kWBytes + (columns(g.n, true) / 2 + C::kBox - 1) / C::kBox * C::kBox * 128);
             }
             ok = wait(C::kInt8 ? sm.x_empty(r.i) : sm.w_empty(r.i), r.phase ^ 1, &s.abort, kErrRing);
             if (!ok) return;
@@ -728,7 +744,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             while (ok && walk.next(g)) {
                 const int c1 = g.k1 * C::kChunksPerBlock;
                 // a pair's CTA has half the tile's columns
-                const int half = ((g.n + 15) & ~15) / 2, first = g.t0 + rank * half;
+                const int half = columns(g.n, C::kPair) / 2, first = g.t0 + rank * half;
                 const int boxes = (half + C::kBox - 1) / C::kBox;
                 for (int c = g.k0 * C::kChunksPerBlock; c < c1; c += C::kChunks) {
                     ok = wait(sm.x_empty(r.i), r.phase ^ 1, &s.abort, kErrRing);
@@ -780,10 +796,10 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
             while (ok && walk.next(g)) {
                 ok = wait(sm.d_empty(dr.i), dr.phase ^ 1, &s.abort, kErrAccumulator);
                 if (!ok) break;
-                const int n16 = (g.n + 15) & ~15;
+                const int cols = columns(g.n, C::kPair);
                 const uint32_t d = tmem + dr.i * TN;
                 constexpr int kM = C::kPair ? 2 * kRows : kRows;
-                const uint32_t idesc = C::kInt8 ? ptx::idesc_s8(kM, n16) : ptx::idesc_f16(kM, n16);
+                const uint32_t idesc = C::kInt8 ? ptx::idesc_s8(kM, cols) : ptx::idesc_f16(kM, cols);
                 uint32_t add = 0;
                 for (int k = g.k0; k < g.k1; k += C::kStepBlocks) {
                     if constexpr (C::kInt8) ok = wait(sm.x_full(r.i), r.phase, &s.abort, kErrRing);
@@ -1191,7 +1207,7 @@ int launch(Params p, const void* x, const void* w, int grid, cudaStream_t stream
 int64_t launch_time(const Params& p, int TN, int grid)
 {
     const TileCost cost = tile_cost(TN);
-    const int64_t pair = TN > 64 ? 2 : 1, P = std::max<int64_t>(grid / pair, 1);
+    const int64_t pair = is_pair(TN) ? 2 : 1, P = std::max<int64_t>(grid / pair, 1);
     // an expert's last tile is half full on average
     const int64_t columns = p.E == 1 ? ((int64_t)p.T + TN - 1) / TN
                                      : std::max<int64_t>(std::min(p.E, p.T), p.T / TN + p.E / 2);
@@ -1385,6 +1401,12 @@ extern "C" int skinny_int8_gemm(const void* q, const float* row_scale, int64_t M
     if (const int rc = current_device(&sms)) return rc;
     if (const int rc = set_workspace(&p, workspace, workspace_bytes, sms)) return rc;
     return launch_any<kFmtInt8, false>(p, q, w, M, sms, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int skinny_debug_tile_columns(int width, int rows)
+{
+    if (width != 16 && width != 32 && width != 64 && width != 128 && width != 192 && width != 256) return -1;
+    return rows >= 1 && rows <= width ? columns(rows, is_pair(width)) : -1;
 }
 
 extern "C" int skinny_tile_device_error(int clear, unsigned* flags)

@@ -437,6 +437,12 @@ int skinny_int8_gemm(const void* q, const float* row_scale, int64_t M, int64_t K
  * CTA's partial sums).  After a call that set it, zero-fill the workspace. */
 int skinny_tile_device_error(int clear, unsigned* flags);
 
+/* Test hook (host only, no CUDA call): the columns of the matrix instruction
+ * for a tile of `width` columns that holds `rows` tokens, or -1 if there is no
+ * such tile.  Tiles of more than 64 columns are computed by pairs of CTAs,
+ * whose instruction takes its columns in steps of 32. */
+int skinny_debug_tile_columns(int width, int rows);
+
 /* ------------------------------------------------------------------------
  * Verification of drafted tokens.
  * ---------------------------------------------------------------------- */
