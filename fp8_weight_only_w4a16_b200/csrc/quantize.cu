@@ -28,8 +28,8 @@ struct Raw {
     __device__ __forceinline__ void load(const void* x, int64_t i)
     {
         const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + i * (F32 ? 4 : 2));
-        w[0] = p[0];
-        if (F32) w[F32 ? 1 : 0] = p[1];
+        w[0] = ptx::ld_global_v4(p);
+        if (F32) w[F32 ? 1 : 0] = ptx::ld_global_v4(p + 1);
     }
     __device__ __forceinline__ void floats(float (&v)[kVec]) const
     {
@@ -110,14 +110,17 @@ __device__ __forceinline__ uint2 quotients(const float (&x)[kVec], float scale, 
 // otherwise it is read a second time.
 template <bool F32, bool KEEP>
 __global__ void __launch_bounds__(1024)
-    quantize(const void* __restrict__ x, int64_t M, int K, int threads_per_row, int8_t* __restrict__ q,
-             float* __restrict__ row_scale)
+    quantize(const void* x_in, int64_t M, int K, int threads_per_row, int8_t* q, float* row_scale)
 {
     __shared__ uint32_t part[32];
     // The next kernel may start once this one has seen the previous one's end:
     // what it reads early was then written two kernels ago at the latest.
     ptx::pdl_wait_prior_grid();
     ptx::pdl_launch_dependents();
+    // The previous kernel may be writing x until the wait is over: coherent loads, whose
+    // address comes from behind it (x is no __restrict__ parameter, which would allow
+    // read-only loads in front of it).
+    const void* x = ptx::after_wait(static_cast<const uint8_t*>(x_in));
     const int r = threadIdx.x / threads_per_row, t = threadIdx.x % threads_per_row;
     const int64_t m = (int64_t)blockIdx.x * (blockDim.x / threads_per_row) + r;
     const bool live = m < M;
