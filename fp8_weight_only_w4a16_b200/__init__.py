@@ -476,7 +476,7 @@ def binding():
         lib = library()
         module.bind(SkinnyError, *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "skinny_gemm_experts", "skinny_gemm_experts_silu_mul", "skinny_quantize_int8", "skinny_int8_gemm",
-            "skinny_verify_draft")))
+            "skinny_verify_draft", "skinny_experts_packed_bytes")))
         _native = module
     return _native
 

@@ -26,6 +26,7 @@ decltype(&skinny_gemm_experts_silu_mul) f_gemm_experts_silu_mul;
 decltype(&skinny_quantize_int8) f_quantize_int8;
 decltype(&skinny_int8_gemm) f_int8_gemm;
 decltype(&skinny_verify_draft) f_verify_draft;
+decltype(&skinny_experts_packed_bytes) f_experts_packed_bytes;
 PyObject* g_error;      // SkinnyError(status, what)
 
 struct Refused : std::runtime_error {      // becomes a ValueError
@@ -50,6 +51,14 @@ void check(const at::Tensor& t, at::ScalarType type, c10::IntArrayRef shape, con
     if (t.scalar_type() != type || t.sizes() != shape || !t.is_contiguous())
         throw Refused(std::string(what) + " must be a contiguous " + c10::toString(type) + " " + shape_text(shape) +
                       " tensor");
+}
+
+// The same for a buffer of any shape.
+void check_count(const at::Tensor& t, at::ScalarType type, int64_t count, const char* what)
+{
+    if (t.scalar_type() != type || t.numel() != count || !t.is_contiguous())
+        throw Refused(std::string(what) + " must be a contiguous " + c10::toString(type) + " tensor of " +
+                      std::to_string(count) + " elements");
 }
 
 // The device of a call: that of its first tensor; every other one has to be on it.
@@ -83,6 +92,8 @@ struct Workspace {
         if (o == Py_None) return;
         const at::Tensor& t = tensor(o, "workspace");
         on.also(t);
+        // (its bytes are counted from the first one on)
+        if (!t.is_contiguous()) throw Refused("workspace must be contiguous");
         ptr = t.data_ptr();
         bytes = t.nbytes();
     }
@@ -163,6 +174,11 @@ PyObject* gemm_experts(PyObject*, PyObject* const* a, Py_ssize_t n)
         if (x.scalar_type() != at::kHalf || x.dim() != 2 || x.size(1) != K || !x.is_contiguous())
             throw Refused("x must be a contiguous float16 [T, " + std::to_string(K) + "] tensor");
         check(off, at::kInt, {E + 1}, "offsets");
+        // the kernel reads the packed experts and their scales by E, N and K
+        const size_t packed = f_experts_packed_bytes((int)fmt, E, N, K, silu);
+        if (packed == 0) throw Failed{SKINNY_ERR_INVALID_ARG, "packed experts' shape"};
+        check_count(data, at::kByte, (int64_t)packed, "data");
+        check_count(scale, at::kFloat, fmt == SKINNY_FMT_NVFP4 ? E : E * N, "scale");
         const int64_t T = x.size(0), outputs = silu ? N / 2 : N;
         const Device on(x);
         for (const at::Tensor* t : {&data, &scale, &off}) on.also(*t);
@@ -216,7 +232,10 @@ PyObject* gemm_int8(PyObject*, PyObject* const* a, Py_ssize_t n)
     return guarded(n, 8, [&] {
         const at::Tensor &q = tensor(a[1], "q"), &rs = tensor(a[2], "row_scale"), &c = tensor(a[3], "codes"),
                          &cs = tensor(a[4], "channel_scale");
+        if (c.dim() != 2) throw Refused("codes must be a contiguous int8 [N, K] tensor");
         const int64_t N = c.size(0), K = c.size(1);
+        check(c, at::kChar, {N, K}, "codes");
+        check(cs, at::kFloat, {N}, "channel_scale");
         if (q.scalar_type() != at::kChar || q.dim() != 2 || q.size(1) != K || !q.is_contiguous())
             throw Refused("q must be a contiguous int8 [M, " + std::to_string(K) + "] tensor");
         const int64_t M = q.size(0);
@@ -289,17 +308,18 @@ PyObject* verify_draft(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
-// (SkinnyError, addresses of the five functions in the order above)
+// (SkinnyError, addresses of the functions: those above, then skinny_experts_packed_bytes)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return guarded(n, 6, [&] {
-        void* f[5];
-        for (int i = 0; i < 5; ++i) f[i] = PyLong_AsVoidPtr(a[i + 1]);
+    return guarded(n, 7, [&] {
+        void* f[6];
+        for (int i = 0; i < 6; ++i) f[i] = PyLong_AsVoidPtr(a[i + 1]);
         f_gemm_experts = reinterpret_cast<decltype(f_gemm_experts)>(f[0]);
         f_gemm_experts_silu_mul = reinterpret_cast<decltype(f_gemm_experts_silu_mul)>(f[1]);
         f_quantize_int8 = reinterpret_cast<decltype(f_quantize_int8)>(f[2]);
         f_int8_gemm = reinterpret_cast<decltype(f_int8_gemm)>(f[3]);
         f_verify_draft = reinterpret_cast<decltype(f_verify_draft)>(f[4]);
+        f_experts_packed_bytes = reinterpret_cast<decltype(f_experts_packed_bytes)>(f[5]);
         Py_INCREF(a[0]);
         Py_XDECREF(g_error);
         g_error = a[0];
