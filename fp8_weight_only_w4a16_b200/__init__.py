@@ -453,6 +453,9 @@ def device_error(clear: bool = True) -> int:
 
 # ---------------------------------------------------------------------------
 # Products for any number of tokens: experts and 8-bit integers
+#
+# With `stream`, a call runs on that stream, and the outputs that it allocates
+# belong to it, as under torch.cuda.stream(stream).
 # ---------------------------------------------------------------------------
 
 _native = None

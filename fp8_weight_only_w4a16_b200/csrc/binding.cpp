@@ -74,15 +74,29 @@ struct Device {
     }
 };
 
-void* stream_of(PyObject* stream, const Device& on)
-{
-    if (stream == Py_None) return c10::cuda::getCurrentCUDAStream(on.d.index()).stream();
-    PyObject* v = PyObject_GetAttrString(stream, "cuda_stream");
-    if (!v) throw Refused("stream must be a torch.cuda.Stream");
-    void* p = PyLong_AsVoidPtr(v);
-    Py_DECREF(v);
-    return p;
-}
+// The call's device and stream (None: the device's current one), current while
+// this lives.  Outputs are allocated under it: the allocator gives memory to a
+// stream, and a block of another one's may still be read or written by what is
+// pending there.
+struct Current {
+    c10::cuda::OptionalCUDAGuard device;
+    c10::cuda::OptionalCUDAStreamGuard stream;      // (sets the device, too)
+    void* handle;
+    Current(PyObject* given, const Device& on)
+    {
+        if (given == Py_None) {
+            device.set_device(on.d);
+            handle = c10::cuda::getCurrentCUDAStream(on.d.index()).stream();
+            return;
+        }
+        PyObject* v = PyObject_GetAttrString(given, "cuda_stream");
+        if (!v) throw Refused("stream must be a torch.cuda.Stream");
+        handle = PyLong_AsVoidPtr(v);
+        Py_DECREF(v);
+        if (PyErr_Occurred()) throw Refused("stream must be a torch.cuda.Stream");
+        stream.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), on.d.index()));
+    }
+};
 
 struct Workspace {
     void* ptr = nullptr;
@@ -183,13 +197,13 @@ PyObject* gemm_experts(PyObject*, PyObject* const* a, Py_ssize_t n)
         const Device on(x);
         for (const at::Tensor* t : {&data, &scale, &off}) on.also(*t);
         const Workspace ws(a[11], on);
-        const c10::cuda::CUDAGuard guard(on.d);
+        const Current now(a[12], on);
         int code;
         const at::Tensor y = output(a[1], a[10], on, T, outputs, &code);
         status((silu ? f_gemm_experts_silu_mul : f_gemm_experts)(
                    (int)fmt, x.data_ptr(), T, K, static_cast<const int32_t*>(off.data_ptr()), E, data.data_ptr(),
                    static_cast<const float*>(scale.data_ptr()), outputs, y.data_ptr(), code, ws.ptr, ws.bytes,
-                   stream_of(a[12], on)),
+                   now.handle),
                silu ? "skinny_gemm_experts_silu_mul" : "skinny_gemm_experts");
         return THPVariable_Wrap(y);
     });
@@ -211,7 +225,7 @@ PyObject* quantize_int8(PyObject*, PyObject* const* a, Py_ssize_t n)
             check(s, at::kFloat, {M}, "row_scale");
         }
         const Device on(x);
-        const c10::cuda::CUDAGuard guard(on.d);
+        const Current now(a[3], on);
         if (q.defined()) {
             on.also(q);
             on.also(s);
@@ -220,7 +234,7 @@ PyObject* quantize_int8(PyObject*, PyObject* const* a, Py_ssize_t n)
             s = at::empty({M}, at::TensorOptions().dtype(at::kFloat).device(on.d));
         }
         status(f_quantize_int8(x.data_ptr(), x.scalar_type() == at::kFloat ? SKINNY_OUT_F32 : SKINNY_OUT_F16, M, K,
-                               q.data_ptr(), static_cast<float*>(s.data_ptr()), stream_of(a[3], on)),
+                               q.data_ptr(), static_cast<float*>(s.data_ptr()), now.handle),
                "skinny_quantize_int8");
         return pair(q, s);
     });
@@ -243,12 +257,12 @@ PyObject* gemm_int8(PyObject*, PyObject* const* a, Py_ssize_t n)
         const Device on(q);
         for (const at::Tensor* t : {&rs, &c, &cs}) on.also(*t);
         const Workspace ws(a[6], on);
-        const c10::cuda::CUDAGuard guard(on.d);
+        const Current now(a[7], on);
         int code;
         const at::Tensor y = output(a[0], a[5], on, M, N, &code);
         status(f_int8_gemm(q.data_ptr(), static_cast<const float*>(rs.data_ptr()), M, K, c.data_ptr(),
                            static_cast<const float*>(cs.data_ptr()), N, y.data_ptr(), code, ws.ptr, ws.bytes,
-                           stream_of(a[7], on)),
+                           now.handle),
                "skinny_int8_gemm");
         return THPVariable_Wrap(y);
     });
@@ -289,7 +303,7 @@ PyObject* verify_draft(PyObject*, PyObject* const* a, Py_ssize_t n)
         const Device on(p);
         for (const at::Tensor* t : std::initializer_list<const at::Tensor*>{&d, &u, &q, &count, &tokens, &accepted})
             if (t->defined()) on.also(*t);
-        const c10::cuda::CUDAGuard guard(on.d);
+        const Current now(a[7], on);
         if (!tokens.defined()) {
             const auto ints = at::TensorOptions().dtype(at::kInt).device(on.d);
             tokens = at::empty({B, S + 1}, ints);
@@ -302,7 +316,7 @@ PyObject* verify_draft(PyObject*, PyObject* const* a, Py_ssize_t n)
                               static_cast<const float*>(u.data_ptr()),
                               has_count ? static_cast<const int32_t*>(count.data_ptr()) : nullptr, B, S, V,
                               static_cast<int32_t*>(tokens.data_ptr()), static_cast<int32_t*>(accepted.data_ptr()),
-                              stream_of(a[7], on)),
+                              now.handle),
                "skinny_verify_draft");
         return pair(tokens, accepted);
     });
