@@ -190,6 +190,9 @@ def unpack_fp8(packed: np.ndarray, N: int, K: int) -> np.ndarray:
 
 # ---------------------------------------------------------------------------
 # Device GEMMs (torch supplies device memory and the stream)
+#
+# With `stream`, a call runs on that stream, and the outputs that it allocates
+# belong to it, as under torch.cuda.stream(stream).
 # ---------------------------------------------------------------------------
 
 @dataclasses.dataclass
@@ -259,6 +262,17 @@ def _stream_handle(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """An output of a call on `stream`, in that stream's memory: a block of the current stream's
+    may still be read by what is pending there."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def gemm_into(y, x, w, workspace=None, stream=None) -> None:
@@ -341,7 +355,7 @@ def gemm(x, w, out_dtype=None, workspace=None, stream=None):
     """Allocate y and compute y = x . W^T (float16 output unless out_dtype says otherwise)."""
     import torch
 
-    y = torch.empty((x.shape[0], w.N), dtype=out_dtype or torch.float16, device=x.device)
+    y = _empty((x.shape[0], w.N), out_dtype or torch.float16, x.device, stream)
     gemm_into(y, x, w, workspace=workspace, stream=stream)
     return y
 
@@ -408,7 +422,7 @@ def gemm_silu_mul(x, w: "PackedGateUp", out_dtype=None, workspace=None, stream=N
     """Allocate y [M, F] and compute the fused gate+up GEMM with SiLU*mul."""
     import torch
 
-    y = torch.empty((x.shape[0], w.F), dtype=out_dtype or torch.float16, device=x.device)
+    y = _empty((x.shape[0], w.F), out_dtype or torch.float16, x.device, stream)
     gemm_silu_mul_into(y, x, w, workspace=workspace, stream=stream)
     return y
 
@@ -438,8 +452,8 @@ def gemm_argmax(x, w, workspace, stream=None):
     """Allocate and return (idx int32 [M], val float32 [M]): see gemm_argmax_into."""
     import torch
 
-    idx = torch.empty((x.shape[0],), dtype=torch.int32, device=x.device)
-    val = torch.empty((x.shape[0],), dtype=torch.float32, device=x.device)
+    idx = _empty((x.shape[0],), torch.int32, x.device, stream)
+    val = _empty((x.shape[0],), torch.float32, x.device, stream)
     gemm_argmax_into(idx, val, x, w, workspace, stream=stream)
     return idx, val
 
