@@ -145,13 +145,14 @@ struct Row {
     __device__ __forceinline__ double sum4(const float (&a)[4], const float (&b)[4], int v0) const
     {
         // With finite numbers, max(p - q, 0) = max(p, q) - q: one FP32 maximum, and
-        // the conversions.  A sum that is not finite, or the token left out, takes
-        // the way that looks at every element.
-        float all = (a[0] + a[1]) + (a[2] + a[3]);
-        if (Q) all += (b[0] + b[1]) + (b[2] + b[3]);
+        // the conversions.  A sum of magnitudes that is not finite, or the token left
+        // out, takes the way that looks at every element.  (No difference is larger
+        // than that sum, so a finite sum leaves none outside FP32's range.)
+        float all = (fabsf(a[0]) + fabsf(a[1])) + (fabsf(a[2]) + fabsf(a[3]));
+        if (Q) all += (fabsf(b[0]) + fabsf(b[1])) + (fabsf(b[2]) + fabsf(b[3]));
         const unsigned hole = (unsigned)without - (unsigned)v0;      // (only a row without q has one)
         double w[4];
-        if (fabsf(all) < INFINITY && (Q || hole >= 4)) {
+        if (all < INFINITY && (Q || hole >= 4)) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 w[j] = (double)fmaxf(a[j], Q ? b[j] : 0.f);
