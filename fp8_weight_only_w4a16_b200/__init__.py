@@ -107,6 +107,8 @@ def library() -> ctypes.CDLL:
                 "skinny_quantize_int8": (ctypes.c_int, [p, ctypes.c_int, i64, i64, p, p, p]),
                 "skinny_int8_gemm": (ctypes.c_int, [p, p, i64, i64, p, p, i64, p, ctypes.c_int, p, sz, p]),
                 "skinny_tile_device_error": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_uint)]),
+                "skinny_debug_tile_width": (ctypes.c_int, [ctypes.c_int, i64, i64, i64, i64, ctypes.c_int, ctypes.c_int,
+                                                           ctypes.c_int, p]),
                 "skinny_debug_tile_columns": (ctypes.c_int, [ctypes.c_int, ctypes.c_int]),
                 "skinny_verify_draft": (ctypes.c_int, [p, i64, i64, p, i64, i64, ctypes.c_int, p, p, p, i64, i64, i64,
                                                        p, p, p]),

@@ -1218,27 +1218,39 @@ int64_t launch_time(const Params& p, int TN, int grid)
     return std::min(whole, tiles * tile / P + cost.epilogue + cost.exchange);
 }
 
-// Token columns per tile: `rows` is the number a tile would like to hold.
-// Narrow tiles leave the shared memory to the weights' ring (the memory-bound
-// range); wide ones reuse each decoded block more often.
-template <int FMT, bool SILU>
-int launch_any(const Params& p, const void* x, const void* w, int64_t rows, int grid, cudaStream_t stream)
+// Token columns per tile.  Narrow tiles leave the shared memory to the weights'
+// ring (the memory-bound range); wide ones reuse each decoded block more often.
+template <int FMT>
+int tile_width(const Params& p, int grid)
 {
-    if (rows <= 16) return launch<FMT, 16, SILU>(p, x, w, grid, stream);
-    if (rows <= 32) return launch<FMT, 32, SILU>(p, x, w, grid, stream);
-    if (rows <= 64) return launch<FMT, 64, SILU>(p, x, w, grid, stream);
+    constexpr int widest = kWidest<FMT>;
+    // What a tile would like to hold.  Routers load experts unevenly: twice the mean.
+    const int64_t rows = FMT == kFmtInt8 || p.T <= 32 ? p.T : 2 * (((int64_t)p.T + p.E - 1) / p.E);
+    if (rows <= 16) return 16;
+    if (rows <= 32) return 32;
+    if (rows <= 64) return 64;
     // More tokens: a wide tile reads the weights fewer times, a narrower one
     // leaves fewer SMs idle where wide tiles are few.  Of those that do not
     // exceed the tokens, the one with the least time by tile_cost: 200 x 4096
     // with 6000 channels takes 15.8 us with 128 and 18.9 with 256, 2048 x 5120
     // with 34816 channels 460 with 128 and 305 with 256.
-    constexpr int kWide = kWidest<FMT>;
     const int64_t t64 = launch_time(p, 64, grid);
     const int64_t t128 = launch_time(p, 128, grid);
-    const int64_t wide = rows <= 128 ? INT64_MAX : launch_time(p, kWide, grid);
-    if (wide <= t64 && wide <= t128) return launch<FMT, kWide, SILU>(p, x, w, grid, stream);
-    if (t128 <= t64) return launch<FMT, 128, SILU>(p, x, w, grid, stream);
-    return launch<FMT, 64, SILU>(p, x, w, grid, stream);
+    const int64_t wide = rows <= 128 ? INT64_MAX : launch_time(p, widest, grid);
+    if (wide <= t64 && wide <= t128) return widest;
+    return t128 <= t64 ? 128 : 64;
+}
+
+template <int FMT, bool SILU>
+int launch_any(const Params& p, const void* x, const void* w, int grid, cudaStream_t stream)
+{
+    switch (tile_width<FMT>(p, grid)) {
+    case 16: return launch<FMT, 16, SILU>(p, x, w, grid, stream);
+    case 32: return launch<FMT, 32, SILU>(p, x, w, grid, stream);
+    case 64: return launch<FMT, 64, SILU>(p, x, w, grid, stream);
+    case 128: return launch<FMT, 128, SILU>(p, x, w, grid, stream);
+    default: return launch<FMT, kWidest<FMT>, SILU>(p, x, w, grid, stream);
+    }
 }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -1252,7 +1264,21 @@ int check_sizes(int64_t T, int64_t K, int64_t N)
     return SKINNY_OK;
 }
 
-// Fills in the workspace; `tiles` is the most tiles the launch can have.
+// Fills in the sizes; SILU*mul has half as many outputs as weight rows.
+int set_sizes(Params* p, int64_t T, int64_t K, int64_t N, int64_t E, bool silu)
+{
+    p->T = (int)T;
+    p->N = (int)N;
+    p->K = (int)K;
+    p->E = (int)E;
+    p->outputs = (int)(silu ? N / 2 : N);
+    p->G = (p->outputs + (silu ? 63 : kRows - 1)) / (silu ? 64 : kRows);
+    p->C = (int)((K + kBlockK - 1) / kBlockK);
+    // the running number of tiles is a 32-bit count
+    return (T / 16 + E) * (int64_t)p->G < (int64_t(1) << 31) ? SKINNY_OK : SKINNY_ERR_UNSUPPORTED;
+}
+
+// Fills in the workspace.
 int set_workspace(Params* p, void* workspace, size_t bytes, int sms)
 {
     p->partials = nullptr;
@@ -1283,27 +1309,17 @@ int experts(int fmt, const void* x, int64_t T, int64_t K, const int32_t* offsets
     p.scale = scale;
     p.offsets = offsets;
     p.y = y;
-    p.T = (int)T;
-    p.N = (int)N;
-    p.K = (int)K;
-    p.E = (int)E;
-    p.outputs = (int)(silu ? N / 2 : N);
-    p.G = (p.outputs + (silu ? 63 : kRows - 1)) / (silu ? 64 : kRows);
-    p.C = (int)((K + kBlockK - 1) / kBlockK);
     p.out_f32 = out_dtype == SKINNY_OUT_F32;
-    // the running number of tiles is a 32-bit count
-    if ((T / 16 + E) * (int64_t)p.G >= (int64_t(1) << 31)) return SKINNY_ERR_UNSUPPORTED;
+    if (const int rc = set_sizes(&p, T, K, N, E, silu)) return rc;
     int sms = 0;
     if (const int rc = current_device(&sms)) return rc;
     if (const int rc = set_workspace(&p, workspace, workspace_bytes, sms)) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // Routers load experts unevenly: twice the mean.
-    const int64_t rows = T <= 32 ? T : 2 * ((T + E - 1) / E);
     if (fmt == SKINNY_FMT_NVFP4)
-        return silu ? launch_any<SKINNY_FMT_NVFP4, true>(p, x, nullptr, rows, sms, st)
-                    : launch_any<SKINNY_FMT_NVFP4, false>(p, x, nullptr, rows, sms, st);
-    return silu ? launch_any<SKINNY_FMT_FP8, true>(p, x, nullptr, rows, sms, st)
-                : launch_any<SKINNY_FMT_FP8, false>(p, x, nullptr, rows, sms, st);
+        return silu ? launch_any<SKINNY_FMT_NVFP4, true>(p, x, nullptr, sms, st)
+                    : launch_any<SKINNY_FMT_NVFP4, false>(p, x, nullptr, sms, st);
+    return silu ? launch_any<SKINNY_FMT_FP8, true>(p, x, nullptr, sms, st)
+                : launch_any<SKINNY_FMT_FP8, false>(p, x, nullptr, sms, st);
 }
 
 bool experts_shape(int fmt, int64_t E, int64_t N, int64_t K, int gate_up, int64_t* G, int64_t* C)
@@ -1389,18 +1405,29 @@ extern "C" int skinny_int8_gemm(const void* q, const float* row_scale, int64_t M
     p.scale = channel_scale;
     p.row_scale = row_scale;
     p.y = y;
-    p.T = (int)M;
-    p.N = p.outputs = (int)N;
-    p.K = (int)K;
-    p.E = 1;
-    p.G = (int)((N + kRows - 1) / kRows);
-    p.C = (int)((K + kBlockK - 1) / kBlockK);
     p.out_f32 = out_dtype == SKINNY_OUT_F32;
-    if ((M / 16 + 1) * (int64_t)p.G >= (int64_t(1) << 31)) return SKINNY_ERR_UNSUPPORTED;
+    if (const int rc = set_sizes(&p, M, K, N, 1, false)) return rc;
     int sms = 0;
     if (const int rc = current_device(&sms)) return rc;
     if (const int rc = set_workspace(&p, workspace, workspace_bytes, sms)) return rc;
-    return launch_any<kFmtInt8, false>(p, q, w, M, sms, static_cast<cudaStream_t>(stream));
+    return launch_any<kFmtInt8, false>(p, q, w, sms, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int skinny_debug_tile_width(int fmt, int64_t T, int64_t K, int64_t N, int64_t E, int gate_up,
+                                       int workspace, int sms, int* width)
+{
+    const bool int8 = fmt == -1, silu = gate_up != 0;
+    if (!width || sms <= 0 || (!int8 && fmt != SKINNY_FMT_NVFP4 && fmt != SKINNY_FMT_FP8)) return SKINNY_ERR_INVALID_ARG;
+    if (T == 0 || E <= 0 || (int8 && (E != 1 || silu)) || (silu && N % 2 != 0)) return SKINNY_ERR_INVALID_ARG;
+    if (const int rc = check_sizes(T, K, N)) return rc;
+    if (E > kMaxExperts || (int8 && K > SKINNY_MAX_INT8_K)) return SKINNY_ERR_UNSUPPORTED;
+    Params p{};
+    if (const int rc = set_sizes(&p, T, K, N, E, silu)) return rc;
+    unsigned there;      // (only whether there is a workspace counts)
+    p.partials = workspace ? &there : nullptr;
+    *width = int8 ? tile_width<kFmtInt8>(p, sms)
+             : fmt == SKINNY_FMT_NVFP4 ? tile_width<SKINNY_FMT_NVFP4>(p, sms) : tile_width<SKINNY_FMT_FP8>(p, sms);
+    return SKINNY_OK;
 }
 
 extern "C" int skinny_debug_tile_columns(int width, int rows)

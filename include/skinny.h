@@ -343,8 +343,8 @@ int skinny_debug_static_workspace_address(void** addr);
  *     along K over all SMs.  It must not be shared by calls that can run at
  *     the same time, and the residency note of skinny_workspace_bytes applies.
  *   - Sums are FP32 (int8: exact 32-bit integers) in an order that depends on
- *     the sizes, the device and (experts) the row counts only, so results are
- *     bitwise reproducible.
+ *     the sizes, the device, whether a workspace is given and (experts) the row
+ *     counts only, so results are bitwise reproducible.
  *   - K is a multiple of 16, K <= 2^20, N <= 2^24; larger sizes and products
  *     of sizes past the tile counter's 31 bits return SKINNY_ERR_UNSUPPORTED.
  * ---------------------------------------------------------------------- */
@@ -436,6 +436,14 @@ int skinny_int8_gemm(const void* q, const float* row_scale, int64_t M, int64_t K
  * as skinny_device_error (1 = a ring slot, 2 = an accumulator, 4 = another
  * CTA's partial sums).  After a call that set it, zero-fill the workspace. */
 int skinny_tile_device_error(int clear, unsigned* flags);
+
+/* Test hook (host only, no CUDA call): *width receives the token columns of a
+ * tile (16, 32, 64, 128, or the widest: 192, int8 256) that a call of these
+ * sizes takes on a device with `sms` SMs.  fmt: a skinny_format, or -1 for the
+ * int8 product (T = M, E = 1); N: weight rows (gate_up: 2F); workspace:
+ * whether one is given.  Errors: as of the call. */
+int skinny_debug_tile_width(int fmt, int64_t T, int64_t K, int64_t N, int64_t E, int gate_up, int workspace, int sms,
+                            int* width);
 
 /* Test hook (host only, no CUDA call): the columns of the matrix instruction
  * for a tile of `width` columns that holds `rows` tokens, or -1 if there is no
