@@ -169,6 +169,13 @@ struct Cfg {
     static_assert(kChunkBytes % 1024 == 0 && kWBytes % 1024 == 0 && kBox * 128 % 1024 == 0,
                   "swizzled tiles start on 1024 bytes");
     static_assert(kXStages >= 3 && kWStages >= 3, "rings");
+    // A group that fills its stage again waits by parity for the token slot of its
+    // last step, kGroups steps ago: the ring may not have come round in between.
+    static_assert(kGroups <= kXStages, "a group's last token slot is in use again");
+    // Two groups are what has been run and tested.  A version with three faulted
+    // when the schedule still kept arrays of 16 entries per warp and the lanes of a
+    // warp left their waits one by one in front of the tensor-memory instructions.
+    static_assert(kInt8 || kGroups == 2, "groups of decoder warps");
     static_assert(columns(TN, kPair) == TN, "a full tile has no columns to spare");
 };
 
