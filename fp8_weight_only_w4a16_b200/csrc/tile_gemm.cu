@@ -414,7 +414,8 @@ struct Shared {
     __device__ uint8_t* x(int i) const { return base + C::kXOff + i * C::kXBytes; }
     __device__ uint8_t* w(int i) const { return base + C::kWOff + i * C::kWBytes; }
     __device__ uint64_t* bars() const { return reinterpret_cast<uint64_t*>(base + C::kBarOff); }
-    // full: the copies have landed.  x_empty: the step's matrix instructions are
+    // full: the copies have landed (a pair's tokens: those of both CTAs, in the
+    // leader's x_full, as the instruction reads both).  x_empty: the step's matrix instructions are
     // done (which also frees the decoded stage that they read, and int8's weights).
     __device__ uint64_t* x_full(int i) const { return bars() + i; }
     __device__ uint64_t* x_empty(int i) const { return bars() + C::kXStages + i; }
@@ -769,15 +770,14 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                                                  sm.x_full(r.i), pol);
                         }
                     } else {
-                        if (!C::kInt8)
-                            ptx::mbar_arrive_expect_tx(sm.x_full(r.i), C::kChunks * boxes * C::kBox * 128);
+                        // both CTAs' copies report to the leader's barrier (int8: the W producer announces them)
+                        if (!C::kInt8 && leader)
+                            ptx::mbar_arrive_expect_tx(sm.x_full(r.i), 2 * C::kChunks * boxes * C::kBox * 128);
                         for (int h = 0; h < C::kChunks; ++h)
                             for (int b = 0; b < boxes; ++b) {
                                 uint8_t* dst = sm.x(r.i) + h * C::kChunkBytes + b * C::kBox * 128;
-                                const int col = (c + h) * kChunkK, at = first + b * C::kBox;
-                                if constexpr (C::kInt8)
-                                    ptx::tma_load_2d_pair(dst, &x_map, col, at, ptx::leader_addr(sm.x_full(r.i)), pol);
-                                else ptx::tma_load_2d(dst, &x_map, col, at, sm.x_full(r.i), pol);
+                                ptx::tma_load_2d_pair(dst, &x_map, (c + h) * kChunkK, first + b * C::kBox,
+                                                      ptx::leader_addr(sm.x_full(r.i)), pol);
                             }
                     }
                     r.step(C::kXStages);
@@ -882,8 +882,8 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                         if (lane == 0) ptx::mbar_arrive(sm.w_empty(wr.i));
                         ptx::tmem_wait_st();
                         ptx::tc_fence_before();
-                        // one warp waits for the tokens too, on the MMA thread's behalf
-                        if ((warp & 3) == 0) ok = wait_warp(sm.x_full(xr.i), xr.phase, &s.abort, kErrRing);
+                        // one warp (a pair's: of the leader) waits for the tokens too, on the MMA thread's behalf
+                        if ((warp & 3) == 0 && leader) ok = wait_warp(sm.x_full(xr.i), xr.phase, &s.abort, kErrRing);
                         if (!ok) break;
                         __syncwarp();
                         if (lane == 0) {
@@ -1029,7 +1029,7 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
         // A wait gave up: copies and matrix instructions may still be in
         // flight.  Let them end before the memory they use is given up.
         if (warp == 0 && !C::kInt8) drain(r, issued, C::kWStages, sm.w_full(0));
-        if (warp == (C::kInt8 ? 0 : 1) && (leader || !C::kInt8)) drain(r, issued, C::kXStages, sm.x_full(0));
+        if (warp == (C::kInt8 ? 0 : 1) && leader) drain(r, issued, C::kXStages, sm.x_full(0));
         if (warp == 2) {
             ptx::tc_commit<C::kPair>(sm.drained());
             ptx::mbar_wait(sm.drained(), 0, kWaitLimitNs);
