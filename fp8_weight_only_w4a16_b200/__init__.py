@@ -109,6 +109,7 @@ def library() -> ctypes.CDLL:
                 "skinny_tile_device_error": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_uint)]),
                 "skinny_debug_tile_width": (ctypes.c_int, [ctypes.c_int, i64, i64, i64, i64, ctypes.c_int, ctypes.c_int,
                                                            ctypes.c_int, p]),
+                "skinny_debug_tile_rings": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, p]),
                 "skinny_debug_tile_columns": (ctypes.c_int, [ctypes.c_int, ctypes.c_int]),
                 "skinny_verify_draft": (ctypes.c_int, [p, i64, i64, p, i64, i64, ctypes.c_int, p, p, p, i64, i64, i64,
                                                        p, p, p]),

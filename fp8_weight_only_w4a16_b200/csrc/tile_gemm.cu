@@ -159,6 +159,16 @@ struct Cfg {
     static constexpr int kWStages = kInt8 ? at_most(kBudget / (kWBytes + kXBytes), 12)
                                           : at_most((kBudget - 3 * kXBytes) / kWBytes, kWTarget / kWBytes);
     static constexpr int kXStages = kInt8 ? kWStages : at_most((kBudget - kWStages * kWBytes) / kXBytes, 12);
+    // A group waits by parity for the copy of its step into a weight slot, which
+    // is right only if the copy before it into that slot, kWStages steps ago, is
+    // known to have landed: a wait that is a whole phase early passes.  A group
+    // knows the copies of its own steps, and of every step up to kGroups before
+    // its last one (it has waited for their matrix instructions), so the ring has
+    // to hold 2 * kGroups steps, or a whole number of the groups' turns.  Where
+    // shared memory has no room for it, a group first waits until its step's token
+    // slot is free: the step kXStages ago is then done, and all before it.
+    static constexpr bool kShortRing = kGroups > 0 && kWStages < 2 * kGroups && kWStages % kGroups != 0;
+    static_assert(!kShortRing || kXStages <= kWStages, "a free token slot does not tell that the weight slot's last copy landed");
     static constexpr int kXOff = 0;
     static constexpr int kWOff = kXStages * kXBytes;
     static constexpr int kBarOff = kWOff + kWStages * kWBytes;
@@ -856,6 +866,10 @@ __global__ void __launch_bounds__(Cfg<FMT, TN>::kThreads, 1)
                 for (int k = g.k0; k < g.k1; k += C::kStepBlocks) {
                     if (turn == 0) {
                         turn = C::kGroups;
+                        if constexpr (C::kShortRing) {
+                            ok = wait_warp(sm.x_empty(xr.i), xr.phase ^ 1, &s.abort, kErrRing);
+                            if (!ok) break;
+                        }
                         ok = wait_warp(sm.w_full(wr.i), wr.phase, &s.abort, kErrRing);
                         if (!ok) break;
                         const uint32_t src = ptx::smem_addr(sm.w(wr.i));
@@ -1435,6 +1449,37 @@ extern "C" int skinny_debug_tile_width(int fmt, int64_t T, int64_t K, int64_t N,
     *width = int8 ? tile_width<kFmtInt8>(p, sms)
              : fmt == SKINNY_FMT_NVFP4 ? tile_width<SKINNY_FMT_NVFP4>(p, sms) : tile_width<SKINNY_FMT_FP8>(p, sms);
     return SKINNY_OK;
+}
+
+namespace {
+template <int FMT, int TN>
+int rings(int* out)
+{
+    using C = Cfg<FMT, TN>;
+    out[0] = C::kWStages;
+    out[1] = C::kXStages;
+    out[2] = C::kGroups;
+    out[3] = C::kShortRing;
+    return SKINNY_OK;
+}
+
+template <int FMT>
+int rings_of(int width, int* out)
+{
+    return width == 16    ? rings<FMT, 16>(out)
+           : width == 32  ? rings<FMT, 32>(out)
+           : width == 64  ? rings<FMT, 64>(out)
+           : width == 128 ? rings<FMT, 128>(out)
+           : width == kWidest<FMT> ? rings<FMT, kWidest<FMT>>(out) : SKINNY_ERR_INVALID_ARG;
+}
+}  // namespace
+
+extern "C" int skinny_debug_tile_rings(int fmt, int width, int* out)
+{
+    if (!out) return SKINNY_ERR_INVALID_ARG;
+    return fmt == -1                  ? rings_of<kFmtInt8>(width, out)
+           : fmt == SKINNY_FMT_NVFP4 ? rings_of<SKINNY_FMT_NVFP4>(width, out)
+           : fmt == SKINNY_FMT_FP8   ? rings_of<SKINNY_FMT_FP8>(width, out) : SKINNY_ERR_INVALID_ARG;
 }
 
 extern "C" int skinny_debug_tile_columns(int width, int rows)

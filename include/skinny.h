@@ -445,6 +445,12 @@ int skinny_tile_device_error(int clear, unsigned* flags);
 int skinny_debug_tile_width(int fmt, int64_t T, int64_t K, int64_t N, int64_t E, int gate_up, int workspace, int sms,
                             int* width);
 
+/* Test hook (host only, no CUDA call): of the kernel of fmt (as above) and
+ * width, out[0] weight slots, out[1] token slots, out[2] groups of decoder
+ * warps, out[3] whether a group waits for a free token slot before it waits for
+ * its weights.  SKINNY_OK or INVALID_ARG. */
+int skinny_debug_tile_rings(int fmt, int width, int* out);
+
 /* Test hook (host only, no CUDA call): the columns of the matrix instruction
  * for a tile of `width` columns that holds `rows` tokens, or -1 if there is no
  * such tile.  Tiles of more than 64 columns are computed by pairs of CTAs,
