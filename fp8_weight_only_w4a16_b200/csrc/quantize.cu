@@ -6,7 +6,7 @@
 // and the rounding, so x is read once (2 or 4 bytes an element) and q written
 // once (1 byte).  Bound by HBM for FP32 rows, by the arithmetic of eight
 // elements a thread for FP16 ones, and by latency for a few rows.  On a B200:
-// 8192 x 5120 in 33 us from FP32 (6.4 TB/s) and 31 us from FP16 (4.0 TB/s), one
+// 8192 x 5120 in 33 us from FP32 (6.4 TB/s) and 32 us from FP16 (4.0 TB/s), one
 // row in 2.4 us.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

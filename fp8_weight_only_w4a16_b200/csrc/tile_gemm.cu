@@ -28,20 +28,22 @@
 // is rounded once.
 //
 // What bounds it, and what it measured on a B200 (6.46 TB/s copy, 1708 TFLOP/s
-// bf16; back-to-back launches in a CUDA graph, weights from HBM):
-//   few rows, FP8     HBM: 64 rows over 128 experts of 5120 x 1408, 49 to 53 us
-//                     (5.9 to 6.4 TB/s).
+// bf16 in a burst, 1437 sustained; back-to-back launches in a CUDA graph,
+// weights from HBM):
+//   few rows, FP8     HBM: 64 rows over 128 experts of 5120 x 1408, 46 to 54 us
+//                     for the 36 to 49 experts that they hit (6.0 to 6.5 TB/s).
 //   few rows, NVFP4   the decoders: 64 rows over 128 experts of 2816 x 5120,
-//                     65 us (5.4 TB/s); a block takes its two groups ~430
-//                     clocks, HBM ~390.
-//   many rows         the tensor cores under the power limit: 16387 rows over
-//                     32 experts of 2816 x 5120, 346 to 390 us (1.21 to 1.37
-//                     PFLOP/s); int8 2048 x 34816 x 5120, 290 to 318 us (2.3
-//                     to 2.5 POP/s, at 1.1 to 1.3 GHz).
+//                     61 to 74 us (4.7 to 5.4 TB/s); a block takes its two
+//                     groups ~430 clocks, HBM ~390.
+//   many rows         the tensor cores, after some half second under the power
+//                     limit: 16387 rows over 32 experts of 2816 x 5120, 357 us
+//                     at first and 421 at 1.35 GHz (1.32 and 1.12 PFLOP/s); int8
+//                     2048 x 34816 x 5120, 297 us and 357 at 0.96 GHz (2.5 and
+//                     2.0 POP/s).
 //   hundreds of rows  launch, first loads and an epilogue, 6 to 8 us together, and
 //                     the last round's idle SMs: 1003 rows over 32 experts of
-//                     2051 x 2048, 26 us; int8 200 x 6000 x 4096, 15 us.
-//   one token         latency: eight experts of 2816 x 2048 (23 MB) 13 us.
+//                     2051 x 2048, 26 to 31 us; int8 200 x 6000 x 4096, 15 us.
+//   one token         latency: eight experts of 2816 x 2048 (23 MB) 12 to 13 us.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -185,9 +187,8 @@ struct Cfg {
     // A group that fills its stage again waits by parity for the token slot of its
     // last step, kGroups steps ago: the ring may not have come round in between.
     static_assert(kGroups <= kXStages, "a group's last token slot is in use again");
-    // Two groups are what has been run and tested.  A version with three faulted
-    // when the schedule still kept arrays of 16 entries per warp and the lanes of a
-    // warp left their waits one by one in front of the tensor-memory instructions.
+    // Two groups are what has been run and tested.  A version with three faulted on
+    // FP8, whose ring of four slots holds less than two of their turns.
     static_assert(kInt8 || kGroups == 2, "groups of decoder warps");
     static_assert(columns(TN, kPair) == TN, "a full tile has no columns to spare");
 };
