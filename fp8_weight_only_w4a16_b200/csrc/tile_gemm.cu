@@ -102,7 +102,7 @@ struct Params {
 
 constexpr int at_most(int a, int b) { return a < b ? a : b; }
 
-// Tiles of more columns than this are computed by pairs of CTAs.
+// Tiles of more than 64 columns are computed by pairs of CTAs.
 __host__ __device__ constexpr bool is_pair(int TN) { return TN > 64; }
 
 // Columns that the matrix instruction of a tile with n tokens has: it takes
@@ -429,8 +429,9 @@ struct Shared {
     __device__ uint8_t* w(int i) const { return base + C::kWOff + i * C::kWBytes; }
     __device__ uint64_t* bars() const { return reinterpret_cast<uint64_t*>(base + C::kBarOff); }
     // full: the copies have landed (a pair's tokens: those of both CTAs, in the
-    // leader's x_full, as the instruction reads both).  x_empty: the step's matrix instructions are
-    // done (which also frees the decoded stage that they read, and int8's weights).
+    // leader's x_full, as the instruction reads both).  x_empty: the step's matrix
+    // instructions are done (which also frees the decoded stage that they read, and
+    // int8's weights).
     __device__ uint64_t* x_full(int i) const { return bars() + i; }
     __device__ uint64_t* x_empty(int i) const { return bars() + C::kXStages + i; }
     __device__ uint64_t* w_full(int i) const { return bars() + 2 * C::kXStages + i; }
